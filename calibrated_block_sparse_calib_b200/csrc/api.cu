@@ -22,6 +22,9 @@
 #include "select.cuh"
 #include "intervals.cuh"
 #include "repeat_sim.cuh"
+#include "transpose.cuh"
+#include "attn_bwd.cuh"
+#include "kv_cache.cuh"
 
 namespace {
 
@@ -300,6 +303,161 @@ calib_status launch_sim(const CUtensorMap& tk, const calib::SimParams& p, int gr
     return launch_status();
 }
 
+// ---- gradients ---------------------------------------------------------------------
+// Workspace of sparse_attn_bwd(_repeat): row statistics over whole blocks, dO as bf16 (fp32 in and
+// out only), and the anchors' rows of Q and dO (repeat heads only).
+struct BwdSpace {
+    size_t stats, do16, qa, doa, total;
+};
+BwdSpace bwd_space(int H, int N, int D, int B, long long n_anchor, bool io_f32) {
+    auto up = [](size_t x) { return (x + 255) & ~static_cast<size_t>(255); };
+    BwdSpace w{};
+    const size_t rows = static_cast<size_t>(cdiv(N, B)) * B;
+    w.do16 = up(H * rows * sizeof(float2));
+    w.qa = w.do16 + (io_f32 ? up(static_cast<size_t>(H) * N * D * 2) : 0);
+    const size_t anchors = n_anchor ? up(static_cast<size_t>(H) * n_anchor * D * 2) : 0;
+    w.doa = w.qa + anchors;
+    w.total = w.doa + anchors;
+    return w;
+}
+
+template <int D, int BLK>
+calib_status launch_bwd(const calib::BwdParams& p, cudaStream_t st) {
+    const int rows = p.geo.nq * BLK;
+    const long long threads = static_cast<long long>(p.geo.H) * rows * (D / 8);
+    calib::bwd_prepare_kernel<D><<<static_cast<int>((threads + 255) / 256), 256, 0, st>>>(p, rows);
+    if (calib_status s = launch_status()) return s;
+    calib::bwd_simple_kernel<D, BLK, false><<<dim3(p.geo.nq * (BLK / 8), p.geo.H), 256, 0, st>>>(p);
+    if (calib_status s = launch_status()) return s;
+    calib::bwd_simple_kernel<D, BLK, true><<<dim3(p.geo.nk * (BLK / 8), p.geo.H), 256, 0, st>>>(p);
+    return launch_status();
+}
+
+calib_status bwd_common(const void* q, const void* k, const void* v, const void* o, const void* dout,
+                        const float* lse, void* dq, void* dk, void* dv, int H, int N, int D, float scale,
+                        const calib_block_list* list, const calib_block_list* list_t, const uint32_t* repeat_bits,
+                        int F, int Hl, int Wl, int n_text, int stride, uint32_t flags, void* workspace,
+                        int64_t workspace_bytes, void* stream) {
+    if (!dq || !dk || !dv || !lse || !dout || !workspace || !list_t || !list_t->row_ptr || !list_t->col_idx)
+        return CALIB_ERR_INVALID;
+    if (flags & ~(CALIB_ATTN_OUT_F32 | CALIB_ATTN_GRAD_F32)) return CALIB_ERR_INVALID;
+    for (const void* x : {static_cast<const void*>(dq), static_cast<const void*>(dk), static_cast<const void*>(dv), dout,
+                          static_cast<const void*>(workspace)})
+        if (!aligned16(x)) return CALIB_ERR_INVALID;
+    AttnCall c;
+    if (calib_status s = attn_prepare(q, k, v, const_cast<void*>(o), const_cast<float*>(lse), H, N, D, scale, list,
+                                      repeat_bits, F, Hl, Wl, n_text, stride, flags & CALIB_ATTN_OUT_F32, &c))
+        return s;
+    if (list_t->H != H || list_t->nq != list->nk || list_t->nk != list->nq || list_t->block != list->block)
+        return CALIB_ERR_INVALID;
+    // every row of dq, dk and dv is written: a work order covers all rows
+    if ((list->work && list->n_work != H * list->nq) || (list_t->work && list_t->n_work != H * list_t->nq))
+        return CALIB_ERR_INVALID;
+    const BwdSpace w = bwd_space(H, N, D, c.B, repeat_bits ? c.p.n_anchor : 0, c.p.out_f32);
+    if (workspace_bytes < static_cast<int64_t>(w.total)) return CALIB_ERR_INVALID;
+    char* base = static_cast<char*>(workspace);
+    calib::BwdParams p{};
+    p.q = static_cast<const __nv_bfloat16*>(q);
+    p.k = static_cast<const __nv_bfloat16*>(k);
+    p.v = static_cast<const __nv_bfloat16*>(v);
+    p.o = o;
+    p.dout = dout;
+    p.lse = lse;
+    p.dq = dq; p.dk = dk; p.dv = dv;
+    p.stats = reinterpret_cast<float2*>(base + w.stats);
+    p.io_f32 = c.p.out_f32;
+    p.do16 = p.io_f32 ? reinterpret_cast<__nv_bfloat16*>(base + w.do16)
+                      : static_cast<__nv_bfloat16*>(const_cast<void*>(dout));
+    p.qa = reinterpret_cast<__nv_bfloat16*>(base + w.qa);
+    p.doa = reinterpret_cast<__nv_bfloat16*>(base + w.doa);
+    p.row_ptr = list->row_ptr; p.col_idx = list->col_idx; p.work = list->work; p.n_work = list->n_work;
+    p.t_row_ptr = list_t->row_ptr; p.t_col_idx = list_t->col_idx; p.t_work = list_t->work; p.n_t_work = list_t->n_work;
+    p.geo = c.p;
+    p.scale = scale;
+    p.grad_f32 = (flags & CALIB_ATTN_GRAD_F32) ? 1 : 0;
+    p.timeout_ns = kDefaultTimeoutNs;
+    cudaStream_t st = as_stream(stream);
+    if (D == 128) return c.B == 128 ? launch_bwd<128, 128>(p, st) : launch_bwd<128, 64>(p, st);
+    return c.B == 128 ? launch_bwd<64, 128>(p, st) : launch_bwd<64, 64>(p, st);
+}
+
+// ---- 8-bit cache -------------------------------------------------------------------
+constexpr int kSms = 148;
+
+// Query rows per CTA (8 or 16), CTAs over the rows, and parts that a sequence's keys are split into:
+// enough CTAs to give every SM about two, and no part below 512 keys (two steps for each of a CTA's
+// eight warps).
+struct CachedPlan {
+    int nt, tiles, splits;
+};
+CachedPlan cached_plan(int S, int Hq, int Hkv, int M, int B, int nb) {
+    CachedPlan c;
+    const long long rows = static_cast<long long>(Hq / Hkv) * M;
+    c.nt = rows <= 8 ? 1 : 2;
+    c.tiles = cdiv(rows, 8 * c.nt);
+    const long long base = static_cast<long long>(S) * Hkv * c.tiles;
+    const long long most = std::max<long long>(1, static_cast<long long>(nb) * B / 512);
+    c.splits = static_cast<int>(std::min(most, std::max<long long>(1, (2 * kSms + base - 1) / base)));
+    return c;
+}
+
+// Checks shared by the cache calls; S sequences, pages of B tokens, nb entries per row of the table.
+calib_status cache_args(const void* k, const void* v, const float* ks, const float* vs, const int32_t* table,
+                        const int32_t* lengths, int S, int Hkv, int M, int D, int B, int nb, int64_t pages) {
+    if (!k || !v || !ks || !vs || !table || !lengths) return CALIB_ERR_INVALID;
+    if (!aligned16(k) || !aligned16(v)) return CALIB_ERR_INVALID;
+    for (const void* x : {static_cast<const void*>(ks), static_cast<const void*>(vs), static_cast<const void*>(table),
+                          static_cast<const void*>(lengths)})
+        if (reinterpret_cast<uintptr_t>(x) & 3u) return CALIB_ERR_INVALID;
+    if (S < 1 || Hkv < 1 || M < 1 || nb < 1 || pages < 1) return CALIB_ERR_INVALID;
+    if (B != 64 && B != 128) return CALIB_ERR_INVALID;
+    if (D != 64 && D != 128) return CALIB_ERR_UNSUPPORTED;
+    // token rows of the cache and positions of a sequence are 32-bit numbers
+    if (pages > ((1ll << 31) - 1) / B / Hkv || nb > ((1ll << 31) - 1) / B) return CALIB_ERR_UNSUPPORTED;
+    if (static_cast<long long>(S) * Hkv * M > (1ll << 31) - 1) return CALIB_ERR_UNSUPPORTED;
+    return check_device();
+}
+
+// 2-D view [pages * Hkv * B][D] of the cache's bytes; box = 32 tokens, swizzled over a token's row.
+bool make_cache_tmap(CUtensorMap* map, const void* base, int D, long long rows) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(rows)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(D)};
+    const cuuint32_t box[2] = {static_cast<cuuint32_t>(D), calib::kChunk};
+    const cuuint32_t estr[2] = {1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, int B, int NT>
+calib_status launch_cached(const CUtensorMap& tk, const CUtensorMap& tv, const calib::CachedParams& p, int grid,
+                           cudaStream_t st) {
+    using L = calib::CachedSmem<D>;
+    static_assert(L::BYTES <= 232448, "shared memory budget");
+    auto* fn = calib::cached_attn_kernel<D, B, NT>;
+    if (calib_status s = ensure_smem(reinterpret_cast<const void*>(fn), L::BYTES)) return s;
+    fn<<<grid, calib::kCachedThreads, L::BYTES, st>>>(tk, tv, p);
+    if (calib_status s = launch_status()) return s;
+    if (p.splits == 1) return CALIB_OK;
+    const long long rows = static_cast<long long>(p.S) * p.Hq * p.M;
+    calib::cached_combine_kernel<D><<<static_cast<int>((rows + 3) / 4), 128, 0, st>>>(p, rows);
+    return launch_status();
+}
+
+template <int D, int B>
+calib_status launch_cached_nt(int nt, const CUtensorMap& tk, const CUtensorMap& tv, const calib::CachedParams& p,
+                              int grid, cudaStream_t st) {
+    return nt == 1 ? launch_cached<D, B, 1>(tk, tv, p, grid, st) : launch_cached<D, B, 2>(tk, tv, p, grid, st);
+}
+
+template <int D, int B>
+calib_status launch_write(const calib::CacheWriteParams& p, int grid, cudaStream_t st) {
+    calib::cache_write_kernel<D, B><<<grid, calib::kWriteThreads, 0, st>>>(p);
+    return launch_status();
+}
+
 int rows_grid(long long rows) { return static_cast<int>((rows + 3) / 4); }   // 4 warps per block
 
 }  // namespace
@@ -323,7 +481,7 @@ calib_status calib_device_check(void* stream) {
     if (cudaMemcpyFromSymbol(&v, calib::g_status, sizeof(v)) != cudaSuccess) return CALIB_ERR_CUDA;
     if (v && cudaMemcpyToSymbol(calib::g_status, &zero, sizeof(zero)) != cudaSuccess) return CALIB_ERR_CUDA;
     if (v & calib::STATUS_TIMEOUT) return CALIB_ERR_TIMEOUT;
-    if (v & (calib::STATUS_BAD_ENERGY | calib::STATUS_BAD_LIST)) return CALIB_ERR_INVALID;
+    if (v & (calib::STATUS_BAD_ENERGY | calib::STATUS_BAD_LIST | calib::STATUS_BAD_CACHE)) return CALIB_ERR_INVALID;
     return CALIB_OK;
 }
 
@@ -475,6 +633,134 @@ calib_status calib_intervals_to_csr(const int32_t* iv_ptr, const int16_t* iv_sta
         calib::iv_expand_kernel<<<rows_grid(rows), 128, 0, st>>>(iv_ptr, iv_start, iv_len, rows, row_ptr_out,
                                                                  col_idx_out);
     return launch_status();
+}
+
+calib_status calib_transpose_csr(const int32_t* row_ptr, const int16_t* col_idx, int H, int nq, int nk,
+                                 int32_t* t_row_ptr_out, int16_t* t_col_idx_out, void* stream) {
+    if (!row_ptr || !col_idx || !t_row_ptr_out || !t_col_idx_out) return CALIB_ERR_INVALID;
+    if (H < 1 || nq < 1 || nk < 1 || nq > 32767 || nk > 32767) return CALIB_ERR_INVALID;
+    if (static_cast<long long>(H) * std::max(nq, nk) > (1ll << 31) - 2) return CALIB_ERR_INVALID;
+    if (calib_status s = check_device()) return s;
+    const int bytes = calib::kTransCols * cdiv(nq, 32) * 4;
+    if (bytes > 48 * 1024)
+        if (calib_status s = ensure_smem(reinterpret_cast<const void*>(calib::transpose_csr_kernel), 32 * 1024 * 4)) return s;
+    calib::transpose_csr_kernel<<<H * cdiv(nk, calib::kTransCols), calib::kTransThreads, bytes, as_stream(stream)>>>(
+        row_ptr, col_idx, H, nq, nk, t_row_ptr_out, t_col_idx_out);
+    return launch_status();
+}
+
+calib_status calib_cache_write(const void* k_new, const void* v_new, void* k_cache, void* v_cache, float* k_scale,
+                               float* v_scale, const int32_t* block_table, const int32_t* lengths,
+                               const int32_t* new_lens, int S, int Hkv, int M, int D, int block, int max_blocks,
+                               int64_t pages, void* stream) {
+    if (!k_new || !v_new || !aligned16(k_new) || !aligned16(v_new)) return CALIB_ERR_INVALID;
+    if (reinterpret_cast<uintptr_t>(new_lens) & 3u) return CALIB_ERR_INVALID;
+    if (calib_status s = cache_args(k_cache, v_cache, k_scale, v_scale, block_table, lengths, S, Hkv, M, D, block,
+                                    max_blocks, pages))
+        return s;
+    calib::CacheWriteParams p{};
+    p.k_new = static_cast<const __nv_bfloat16*>(k_new);
+    p.v_new = static_cast<const __nv_bfloat16*>(v_new);
+    p.k = static_cast<uint8_t*>(k_cache);
+    p.v = static_cast<uint8_t*>(v_cache);
+    p.k_scale = k_scale; p.v_scale = v_scale;
+    p.table = block_table; p.lengths = lengths; p.new_lens = new_lens;
+    p.S = S; p.Hkv = Hkv; p.M = M; p.nb = max_blocks; p.pages = static_cast<int>(pages);
+    p.T = std::min(cdiv(M - 1, block) + 1, max_blocks);
+    const long long grid = 2ll * S * Hkv * p.T;
+    if (grid > (1ll << 31) - 1) return CALIB_ERR_UNSUPPORTED;
+    cudaStream_t st = as_stream(stream);
+    const int g = static_cast<int>(grid);
+    if (D == 128) return block == 128 ? launch_write<128, 128>(p, g, st) : launch_write<128, 64>(p, g, st);
+    return block == 128 ? launch_write<64, 128>(p, g, st) : launch_write<64, 64>(p, g, st);
+}
+
+int64_t sparse_attn_cached_workspace(int S, int Hq, int Hkv, int M, int D, int block, int max_blocks) {
+    if (S < 1 || Hkv < 1 || Hq < Hkv || Hq % Hkv || M < 1 || max_blocks < 1 || (block != 64 && block != 128) ||
+        (D != 64 && D != 128) || static_cast<long long>(S) * Hq > (1ll << 31) - 1 ||
+        static_cast<long long>(S) * Hq * M > (1ll << 31) - 1)
+        return -1;
+    const CachedPlan c = cached_plan(S, Hq, Hkv, M, block, max_blocks);
+    return c.splits == 1 ? 0 : static_cast<int64_t>(S) * Hq * M * c.splits * (D * 4 + 8);
+}
+
+calib_status sparse_attn_cached(const void* q, const void* k_cache, const void* v_cache, const float* k_scale,
+                                const float* v_scale, const int32_t* block_table, const int32_t* lengths,
+                                const int32_t* new_lens, void* o, float* lse_opt, int S, int Hq, int Hkv, int M,
+                                int D, int block, int max_blocks, int64_t pages, float scale,
+                                const calib_block_list* list, uint32_t flags, void* workspace,
+                                int64_t workspace_bytes, void* stream) {
+    if (!q || !o || !aligned16(q) || !aligned16(o)) return CALIB_ERR_INVALID;
+    if (flags & ~(CALIB_ATTN_OUT_F32 | CALIB_ATTN_CAUSAL)) return CALIB_ERR_INVALID;
+    if ((reinterpret_cast<uintptr_t>(new_lens) & 3u) || (reinterpret_cast<uintptr_t>(lse_opt) & 3u)) return CALIB_ERR_INVALID;
+    if (!(scale > 0.f) || !std::isfinite(scale)) return CALIB_ERR_INVALID;
+    if (Hkv < 1 || Hq < Hkv || Hq % Hkv) return CALIB_ERR_INVALID;
+    if (calib_status s = cache_args(k_cache, v_cache, k_scale, v_scale, block_table, lengths, S, Hkv, M, D, block,
+                                    max_blocks, pages))
+        return s;
+    if (list && (!list->row_ptr || !list->col_idx || list->H != Hkv || list->nq != S || list->nk != max_blocks ||
+                 list->block != block || max_blocks > 32767))
+        return CALIB_ERR_INVALID;
+    const int64_t need = sparse_attn_cached_workspace(S, Hq, Hkv, M, D, block, max_blocks);
+    if (need < 0) return CALIB_ERR_UNSUPPORTED;
+    if (need > 0 && (!workspace || !aligned16(workspace) || workspace_bytes < need)) return CALIB_ERR_INVALID;
+    const CachedPlan c = cached_plan(S, Hq, Hkv, M, block, max_blocks);
+    const long long grid = static_cast<long long>(S) * Hkv * c.tiles * c.splits;
+    if (grid > (1ll << 31) - 1) return CALIB_ERR_UNSUPPORTED;
+    calib::CachedParams p{};
+    p.q = static_cast<const __nv_bfloat16*>(q);
+    p.k_scale = k_scale; p.v_scale = v_scale;
+    p.table = block_table; p.lengths = lengths; p.new_lens = new_lens;
+    if (list) {
+        p.row_ptr = list->row_ptr;
+        p.col_idx = list->col_idx;
+    }
+    p.o = o;
+    p.lse = lse_opt;
+    p.part_o = static_cast<float*>(workspace);
+    p.part_ml = reinterpret_cast<float2*>(p.part_o + static_cast<size_t>(S) * Hq * M * c.splits * D);
+    p.S = S; p.Hq = Hq; p.Hkv = Hkv; p.G = Hq / Hkv; p.M = M; p.nb = max_blocks; p.pages = static_cast<int>(pages);
+    p.tiles = c.tiles; p.splits = c.splits;
+    p.causal = (flags & CALIB_ATTN_CAUSAL) ? 1 : 0;
+    p.out_f32 = (flags & CALIB_ATTN_OUT_F32) ? 1 : 0;
+    p.scale_log2 = scale * 1.4426950408889634f;
+    p.timeout_ns = kDefaultTimeoutNs;
+    CUtensorMap tk, tv;
+    const long long rows = static_cast<long long>(pages) * Hkv * block;
+    if (!make_cache_tmap(&tk, k_cache, D, rows) || !make_cache_tmap(&tv, v_cache, D, rows)) return CALIB_ERR_CUDA;
+    cudaStream_t st = as_stream(stream);
+    const int g = static_cast<int>(grid);
+    if (D == 128) return block == 128 ? launch_cached_nt<128, 128>(c.nt, tk, tv, p, g, st)
+                                      : launch_cached_nt<128, 64>(c.nt, tk, tv, p, g, st);
+    return block == 128 ? launch_cached_nt<64, 128>(c.nt, tk, tv, p, g, st)
+                        : launch_cached_nt<64, 64>(c.nt, tk, tv, p, g, st);
+}
+
+int64_t sparse_attn_bwd_workspace(int H, int N, int D, int block, int n_anchor, uint32_t flags) {
+    if (H < 1 || N < 1 || (D != 64 && D != 128) || (block != 64 && block != 128) || n_anchor < 0 || n_anchor > N ||
+        static_cast<long long>(H) * N * D >= (1ll << 40) || (flags & ~(CALIB_ATTN_OUT_F32 | CALIB_ATTN_GRAD_F32)))
+        return -1;
+    return static_cast<int64_t>(bwd_space(H, N, D, block, n_anchor, flags & CALIB_ATTN_OUT_F32).total);
+}
+
+calib_status sparse_attn_bwd(const void* q, const void* k, const void* v, const void* o, const void* dout,
+                             const float* lse, void* dq, void* dk, void* dv, int H, int N, int D, float scale,
+                             const calib_block_list* list, const calib_block_list* list_t, uint32_t flags,
+                             void* workspace, int64_t workspace_bytes, void* stream) {
+    return bwd_common(q, k, v, o, dout, lse, dq, dk, dv, H, N, D, scale, list, list_t, nullptr, 1, 1, N, 0, 1, flags,
+                      workspace, workspace_bytes, stream);
+}
+
+calib_status sparse_attn_bwd_repeat(const void* q, const void* k, const void* v, const void* o, const void* dout,
+                                    const float* lse, void* dq, void* dk, void* dv, int H, int D, int F, int Hl,
+                                    int Wl, int n_text, int stride, const uint8_t* head_repeat, float scale,
+                                    const calib_block_list* list, const calib_block_list* list_t, uint32_t flags,
+                                    void* workspace, int64_t workspace_bytes, void* stream) {
+    uint32_t bits[32];
+    int N = 0;
+    if (calib_status s = repeat_geometry(H, F, Hl, Wl, n_text, stride, head_repeat, bits, &N)) return s;
+    return bwd_common(q, k, v, o, dout, lse, dq, dk, dv, H, N, D, scale, list, list_t, bits, F, Hl, Wl, n_text, stride,
+                      flags, workspace, workspace_bytes, stream);
 }
 
 calib_status calib_repeat_similarity(const void* q, const void* k, const float* lse, int H, int N, int D, int block,

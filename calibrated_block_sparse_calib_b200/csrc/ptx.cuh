@@ -14,8 +14,9 @@ namespace calib {
 // TIMEOUT: a bounded wait gave up.  BAD_ENERGY: selection met a negative or non-finite
 // energy (counted as 0).  BAD_LIST: an attention work item named a head or query block
 // outside the call, or a row whose pointers are negative or decreasing, or keep more
-// than nk blocks; the item was skipped.
-enum : uint32_t { STATUS_TIMEOUT = 1u, STATUS_BAD_ENERGY = 2u, STATUS_BAD_LIST = 4u };
+// than nk blocks; the item was skipped.  BAD_CACHE: a cache call met a length or a count of new
+// tokens out of range (that sequence is skipped) or a page outside the cache (that block is).
+enum : uint32_t { STATUS_TIMEOUT = 1u, STATUS_BAD_ENERGY = 2u, STATUS_BAD_LIST = 4u, STATUS_BAD_CACHE = 8u };
 __device__ uint32_t g_status;
 
 __device__ __forceinline__ void raise_status(uint32_t bits) { atomicOr(&g_status, bits); }

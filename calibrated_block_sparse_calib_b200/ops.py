@@ -19,7 +19,7 @@ _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libcalibatt.so")
 
 CALIB_OK, CALIB_ERR_INVALID, CALIB_ERR_UNSUPPORTED, CALIB_ERR_CUDA, CALIB_ERR_TIMEOUT = range(5)
-CALIB_ATTN_OUT_F32 = 1
+CALIB_ATTN_OUT_F32, CALIB_ATTN_GRAD_F32, CALIB_ATTN_CAUSAL = 1, 2, 4
 
 
 class CalibError(RuntimeError):
@@ -61,6 +61,16 @@ _SIGS = {
                               _U32, _I, _P, _P, _P], ctypes.c_int),
     "sparse_attn_fwd_repeat_host": ([_P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _P, _F,
                                      ctypes.POINTER(_BlockListC), _U32, _I, _P, _P, _P], ctypes.c_int),
+    "calib_transpose_csr": ([_P, _P, _I, _I, _I, _P, _P, _P], ctypes.c_int),
+    "sparse_attn_bwd_workspace": ([_I, _I, _I, _I, _I, _U32], ctypes.c_int64),
+    "sparse_attn_bwd": ([_P] * 9 + [_I, _I, _I, _F, ctypes.POINTER(_BlockListC), ctypes.POINTER(_BlockListC), _U32, _P,
+                                    ctypes.c_int64, _P], ctypes.c_int),
+    "sparse_attn_bwd_repeat": ([_P] * 9 + [_I, _I, _I, _I, _I, _I, _I, _P, _F, ctypes.POINTER(_BlockListC),
+                                           ctypes.POINTER(_BlockListC), _U32, _P, ctypes.c_int64, _P], ctypes.c_int),
+    "calib_cache_write": ([_P] * 9 + [_I, _I, _I, _I, _I, _I, ctypes.c_int64, _P], ctypes.c_int),
+    "sparse_attn_cached_workspace": ([_I] * 7, ctypes.c_int64),
+    "sparse_attn_cached": ([_P] * 10 + [_I] * 7 + [ctypes.c_int64, _F, ctypes.POINTER(_BlockListC), _U32, _P,
+                                                   ctypes.c_int64, _P], ctypes.c_int),
     "calib_selftest_wait_timeout": ([_U32, _P], ctypes.c_int),
 }
 
@@ -106,6 +116,14 @@ def _need(t: torch.Tensor, name: str, dtype: torch.dtype, shape=None):
         raise ValueError(f"{name} must be contiguous")
     if shape is not None and tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _on_current_device(**tensors):
+    """The calls launch on the current device's stream, so their tensors have to live there."""
+    dev = torch.cuda.current_device()
+    for name, t in tensors.items():
+        if t is not None and t.device.index != dev:
+            raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
 
 
 def device_check():
@@ -250,6 +268,21 @@ def mask_to_csr(mask: torch.Tensor):
     return row_ptr, col_idx
 
 
+def transpose_csr(row_ptr: torch.Tensor, col_idx: torch.Tensor, H: int, nq: int, nk: int):
+    """(row_ptr int32 [H*nk+1], col_idx int16) of the skip list by key block: for every (head, key
+    block) the ascending query blocks that keep it, with col_idx's capacity."""
+    _need(row_ptr, "row_ptr", torch.int32, (H * nq + 1,))
+    _need(col_idx, "col_idx", torch.int16)
+    _on_current_device(row_ptr=row_ptr, col_idx=col_idx)
+    t_ptr = torch.empty(H * nk + 1, dtype=torch.int32, device=row_ptr.device)
+    t_col = torch.empty_like(col_idx)
+    # an empty list still needs valid pointers
+    src, dst = (col_idx, t_col) if col_idx.numel() else (row_ptr, t_ptr)
+    _check("calib_transpose_csr", lib().calib_transpose_csr(
+        _ptr(row_ptr), _ptr(src), H, nq, nk, _ptr(t_ptr), _ptr(dst), _stream()))
+    return t_ptr, t_col
+
+
 def csr_to_intervals(row_ptr: torch.Tensor, col_idx: torch.Tensor, H: int, nq: int):
     """Runs of consecutive kept blocks per row: (iv_ptr int32 [H*nq+1], starts int16, lengths
     int16), the runs trimmed to their count."""
@@ -371,6 +404,13 @@ class BlockList:
             raise ValueError("malformed skip list")
         return self
 
+    def transpose(self, schedule: bool = True) -> "BlockList":
+        """The same kept blocks by key block (nq and nk exchanged), as sparse_attn_bwd walks them for
+        the gradients of K and V."""
+        rp, ci = transpose_csr(self.row_ptr, self.col_idx, self.H, self.nq, self.nk)
+        work = build_schedule(rp, self.H, self.nk) if schedule else None
+        return BlockList(self.H, self.nk, self.nq, self.block, rp, ci, work)
+
     @staticmethod
     def from_mask(mask: torch.Tensor, block: int, schedule: bool = True) -> "BlockList":
         """Skip list (and longest-first schedule) of a uint8 [H, nq, nk] device mask."""
@@ -433,6 +473,198 @@ def sparse_attn_fwd_repeat(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, bl
     _check("sparse_attn_fwd_repeat", lib().sparse_attn_fwd_repeat(
         _ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), H, D, F, Hl, Wl, n_text, stride,
         ctypes.cast(flags, ctypes.c_void_p), scale, ctypes.byref(cs), oflags, _stream()))
+    return (out, lse) if (return_lse or lse is not None) else out
+
+
+# ----------------------------------------------------------------------------------
+# gradients
+# ----------------------------------------------------------------------------------
+
+def _bwd(name, q, k, v, out, dout, lse, blist, blist_t, scale, grads, grad_dtype, n_anchor, geometry):
+    H, N, D = q.shape
+    for t, n in ((q, "q"), (k, "k"), (v, "v")):
+        _need(t, n, torch.bfloat16, (H, N, D))
+    if out.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError("out must be bf16 or fp32")
+    _need(out, "out", out.dtype, (H, N, D))
+    _need(dout, "dout", out.dtype, (H, N, D))
+    _need(lse, "lse", torch.float32, (H, N))
+    if grad_dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError("gradients are bf16 or fp32")
+    dq, dk, dv = (torch.empty((H, N, D), dtype=grad_dtype, device=q.device) if t is None else t for t in grads)
+    for t, n in ((dq, "dq"), (dk, "dk"), (dv, "dv")):
+        _need(t, n, grad_dtype, (H, N, D))
+    _on_current_device(q=q, k=k, v=v, out=out, dout=dout, lse=lse, dq=dq, dk=dk, dv=dv, row_ptr=blist.row_ptr)
+    if blist_t is None:
+        blist_t = blist.transpose()
+    flags = (CALIB_ATTN_OUT_F32 if out.dtype == torch.float32 else 0) | \
+        (CALIB_ATTN_GRAD_F32 if grad_dtype == torch.float32 else 0)
+    need = lib().sparse_attn_bwd_workspace(H, N, D, blist.block, n_anchor, flags)
+    space = torch.empty(max(1, need), dtype=torch.uint8, device=q.device)
+    cs, ct = blist.c_struct(), blist_t.c_struct()
+    sizes = (H, N, D) if geometry is None else (H, D, *geometry)
+    scale = 1.0 / math.sqrt(D) if scale is None else scale
+    _check(name, getattr(lib(), name)(
+        _ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(dout), _ptr(lse), _ptr(dq), _ptr(dk), _ptr(dv), *sizes, scale,
+        ctypes.byref(cs), ctypes.byref(ct), flags, _ptr(space), space.numel(), _stream()))
+    return dq, dk, dv
+
+
+def sparse_attn_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Tensor, dout: torch.Tensor,
+                    lse: torch.Tensor, blist: BlockList, blist_t: Optional[BlockList] = None,
+                    scale: Optional[float] = None, dq: Optional[torch.Tensor] = None,
+                    dk: Optional[torch.Tensor] = None, dv: Optional[torch.Tensor] = None,
+                    grad_dtype: torch.dtype = torch.bfloat16):
+    """Gradients (dq, dk, dv) of sparse_attn_fwd from its saved output and LSE and the output's
+    gradient.  blist_t is blist.transpose(); without it the list is transposed in the call."""
+    return _bwd("sparse_attn_bwd", q, k, v, out, dout, lse, blist, blist_t, scale, (dq, dk, dv), grad_dtype, 0, None)
+
+
+def sparse_attn_bwd_repeat(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Tensor, dout: torch.Tensor,
+                           lse: torch.Tensor, blist: BlockList, head_repeat: Sequence[bool], F: int, Hl: int, Wl: int,
+                           n_text: int, stride: int, blist_t: Optional[BlockList] = None,
+                           scale: Optional[float] = None, dq: Optional[torch.Tensor] = None,
+                           dk: Optional[torch.Tensor] = None, dv: Optional[torch.Tensor] = None,
+                           grad_dtype: torch.dtype = torch.bfloat16):
+    """Gradients of sparse_attn_fwd_repeat: a repeat head's anchors collect the gradients of the
+    tokens that take their output."""
+    H, N, D = q.shape
+    if N != F * Hl * Wl + n_text:
+        raise ValueError("N must equal F*Hl*Wl + n_text")
+    if len(head_repeat) != H:
+        raise ValueError(f"head_repeat needs one entry per head ({H})")
+    flags = (ctypes.c_uint8 * H)(*[1 if bool(x) else 0 for x in head_repeat])
+    geometry = (F, Hl, Wl, n_text, stride, ctypes.cast(flags, ctypes.c_void_p))
+    return _bwd("sparse_attn_bwd_repeat", q, k, v, out, dout, lse, blist, blist_t, scale, (dq, dk, dv), grad_dtype,
+                anchor_count(F, Hl, Wl, n_text, stride), geometry)
+
+
+class _SparseAttention(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, v, blist, blist_t, scale, out_dtype, repeat):
+        if repeat is None:
+            out, lse = sparse_attn_fwd(q, k, v, blist, scale=scale, return_lse=True, out_dtype=out_dtype)
+        else:
+            out, lse = sparse_attn_fwd_repeat(q, k, v, blist, *repeat, scale=scale, return_lse=True, out_dtype=out_dtype)
+        ctx.save_for_backward(q, k, v, out, lse)
+        ctx.plan = (blist, blist_t, scale, repeat)
+        return out
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dout):
+        q, k, v, out, lse = ctx.saved_tensors
+        blist, blist_t, scale, repeat = ctx.plan
+        with torch.cuda.device(q.device):
+            if repeat is None:
+                g = sparse_attn_bwd(q, k, v, out, dout.contiguous(), lse, blist, blist_t, scale)
+            else:
+                g = sparse_attn_bwd_repeat(q, k, v, out, dout.contiguous(), lse, blist, *repeat, blist_t=blist_t,
+                                           scale=scale)
+        return (*g, None, None, None, None, None)
+
+
+def sparse_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, blist: BlockList,
+                     blist_t: Optional[BlockList] = None, scale: Optional[float] = None,
+                     out_dtype: torch.dtype = torch.bfloat16, repeat: Optional[tuple] = None) -> torch.Tensor:
+    """Block-sparse attention that torch's autograd differentiates (sparse_attn_fwd and
+    sparse_attn_bwd).  blist_t = blist.transpose() saves its computation in every backward pass;
+    repeat = (head_repeat, F, Hl, Wl, n_text, stride) selects spatial-repetition mode.  Differentiable
+    once.  The lists must not change between the forward and the backward pass."""
+    return _SparseAttention.apply(q, k, v, blist, blist_t, scale, out_dtype, repeat)
+
+
+# ----------------------------------------------------------------------------------
+# a key/value cache in 8 bits
+# ----------------------------------------------------------------------------------
+
+@dataclass
+class KVCache:
+    """Paged keys and values in e4m3 with an fp32 scale per page (a block of tokens) and head:
+    k, v [pages, Hkv, B, D], k_scale, v_scale [pages, Hkv]."""
+    k: torch.Tensor
+    v: torch.Tensor
+    k_scale: torch.Tensor
+    v_scale: torch.Tensor
+
+    @staticmethod
+    def allocate(pages: int, Hkv: int, block: int, D: int, device="cuda") -> "KVCache":
+        data = lambda: torch.empty((pages, Hkv, block, D), dtype=torch.float8_e4m3fn, device=device)
+        scale = lambda: torch.zeros((pages, Hkv), dtype=torch.float32, device=device)
+        return KVCache(data(), data(), scale(), scale())
+
+    def check(self):
+        """(pages, Hkv, block, D) of a well-formed cache; raises otherwise."""
+        pages, Hkv, block, D = self.k.shape
+        _need(self.k, "cache.k", torch.float8_e4m3fn)
+        _need(self.v, "cache.v", torch.float8_e4m3fn, self.k.shape)
+        _need(self.k_scale, "cache.k_scale", torch.float32, (pages, Hkv))
+        _need(self.v_scale, "cache.v_scale", torch.float32, (pages, Hkv))
+        return pages, Hkv, block, D
+
+
+def _sequences(block_table, lengths, new_lens, S):
+    _need(block_table, "block_table", torch.int32)
+    if block_table.dim() != 2 or block_table.shape[0] != S:
+        raise ValueError(f"block_table must have shape ({S}, max_blocks), got {tuple(block_table.shape)}")
+    _need(lengths, "lengths", torch.int32, (S,))
+    if new_lens is not None:
+        _need(new_lens, "new_lens", torch.int32, (S,))
+    return block_table.shape[1]
+
+
+def cache_write(cache: KVCache, k_new: torch.Tensor, v_new: torch.Tensor, block_table: torch.Tensor,
+                lengths: torch.Tensor, new_lens: Optional[torch.Tensor] = None) -> KVCache:
+    """Write new tokens k_new, v_new (bf16 [S, Hkv, M, D]) into the cache, in place: slot m of
+    sequence s goes to position lengths[s] - new_lens[s] + m (new_lens: M each by default)."""
+    pages, Hkv, block, D = cache.check()
+    S, M = k_new.shape[0], k_new.shape[2] if k_new.dim() == 4 else 0
+    _need(k_new, "k_new", torch.bfloat16, (S, Hkv, M, D))
+    _need(v_new, "v_new", torch.bfloat16, (S, Hkv, M, D))
+    nb = _sequences(block_table, lengths, new_lens, S)
+    _on_current_device(k_new=k_new, v_new=v_new, cache=cache.k, cache_v=cache.v, k_scale=cache.k_scale,
+                       v_scale=cache.v_scale, block_table=block_table, lengths=lengths, new_lens=new_lens)
+    _check("calib_cache_write", lib().calib_cache_write(
+        _ptr(k_new), _ptr(v_new), _ptr(cache.k), _ptr(cache.v), _ptr(cache.k_scale), _ptr(cache.v_scale),
+        _ptr(block_table), _ptr(lengths), _ptr(new_lens), S, Hkv, M, D, block, nb, pages, _stream()))
+    return cache
+
+
+def sparse_attn_cached(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, lengths: torch.Tensor,
+                       blist: Optional[BlockList] = None, new_lens: Optional[torch.Tensor] = None,
+                       causal: bool = True, scale: Optional[float] = None, out: Optional[torch.Tensor] = None,
+                       lse: Optional[torch.Tensor] = None, return_lse: bool = False,
+                       out_dtype: torch.dtype = torch.bfloat16):
+    """Attention of q (bf16 [S, Hq, M, D]: the last new_lens[s] <= M tokens of each sequence) over the
+    cached keys and values, over all of a sequence's blocks or those that blist (H = Hkv, nq = S,
+    nk = max_blocks) keeps.  O [S, Hq, M, D] in bf16 (or fp32 via out_dtype / an fp32 `out`), and the fp32
+    LSE [S, Hq, M] if requested."""
+    pages, Hkv, block, D = cache.check()
+    if q.dim() != 4:
+        raise ValueError("q must have shape [S, Hq, M, D]")
+    S, Hq, M, _ = q.shape
+    _need(q, "q", torch.bfloat16, (S, Hq, M, D))
+    nb = _sequences(block_table, lengths, new_lens, S)
+    if out is None:
+        out = torch.empty((S, Hq, M, D), dtype=out_dtype, device=q.device)
+    if out.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError("out must be bf16 or fp32")
+    _need(out, "out", out.dtype, (S, Hq, M, D))
+    if return_lse and lse is None:
+        lse = torch.empty((S, Hq, M), dtype=torch.float32, device=q.device)
+    if lse is not None:
+        _need(lse, "lse", torch.float32, (S, Hq, M))
+    _on_current_device(q=q, cache=cache.k, cache_v=cache.v, k_scale=cache.k_scale, v_scale=cache.v_scale,
+                       block_table=block_table, lengths=lengths, new_lens=new_lens, out=out, lse=lse)
+    need = lib().sparse_attn_cached_workspace(S, Hq, Hkv, M, D, block, nb)
+    space = torch.empty(need, dtype=torch.uint8, device=q.device) if need > 0 else None
+    cs = None if blist is None else blist.c_struct()
+    flags = (CALIB_ATTN_OUT_F32 if out.dtype == torch.float32 else 0) | (CALIB_ATTN_CAUSAL if causal else 0)
+    scale = 1.0 / math.sqrt(D) if scale is None else scale
+    _check("sparse_attn_cached", lib().sparse_attn_cached(
+        _ptr(q), _ptr(cache.k), _ptr(cache.v), _ptr(cache.k_scale), _ptr(cache.v_scale), _ptr(block_table),
+        _ptr(lengths), _ptr(new_lens), _ptr(out), _ptr(lse), S, Hq, Hkv, M, D, block, nb, pages, scale,
+        None if cs is None else ctypes.byref(cs), flags, _ptr(space), max(0, need), _stream()))
     return (out, lse) if (return_lse or lse is not None) else out
 
 

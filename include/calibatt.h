@@ -42,7 +42,9 @@ extern "C" {
 #endif
 
 /* Flags of the attention calls. */
-#define CALIB_ATTN_OUT_F32 1u   /* o is fp32 [H, N, D] instead of bf16 */
+#define CALIB_ATTN_OUT_F32 1u   /* o (and dout) is fp32 instead of bf16 */
+#define CALIB_ATTN_GRAD_F32 2u  /* sparse_attn_bwd: dq, dk, dv are fp32 instead of bf16 */
+#define CALIB_ATTN_CAUSAL 4u    /* sparse_attn_cached: a new token sees no later one */
 
 typedef enum calib_status {
     CALIB_OK = 0,
@@ -75,7 +77,8 @@ const char* calib_status_string(calib_status s);
  * wait; CALIB_ERR_INVALID if a selection kernel met a negative or non-finite energy
  * (treated as 0) or an attention kernel met a work item outside the call (head >= H or
  * query block >= nq) or a skip-list row with a negative start, decreasing pointers or
- * more than nk blocks (that item is skipped, its output rows are not written);
+ * more than nk blocks (that item is skipped, its output rows are not written), or a cache
+ * call met a length, a count of new tokens or a page out of range (see those calls);
  * CALIB_ERR_CUDA on a CUDA error; else CALIB_OK. */
 calib_status calib_device_check(void* stream);
 
@@ -296,6 +299,125 @@ calib_status sparse_attn_fwd_repeat(const void* q, const void* k, const void* v,
                                     int n_text, int stride, const uint8_t* head_repeat,
                                     float scale, const calib_block_list* list,
                                     uint32_t flags, void* stream);
+
+/* The skip list by key block: for every (head, key block) the ascending query blocks that
+ * keep it, in the same CSR form with the two block axes exchanged (row h*nk + j of the
+ * output holds i for every j in row h*nq + i of the input).  The gradients of K and V walk
+ * it (sparse_attn_bwd); as a calib_block_list it has nq and nk exchanged, and its work
+ * order is calib_build_schedule(t_row_ptr, H, nk).
+ *   t_row_ptr_out : int32 [H*nk + 1].
+ *   t_col_idx_out : int16 with capacity for every kept block (row_ptr[H*nq]).
+ * Exact integer work, one launch.  nq, nk <= 32767.  A row whose pointers are negative,
+ * decreasing or more than nk apart is left out and reported (calib_device_check). */
+calib_status calib_transpose_csr(const int32_t* row_ptr, const int16_t* col_idx, int H, int nq,
+                                 int nk, int32_t* t_row_ptr_out, int16_t* t_col_idx_out,
+                                 void* stream);
+
+/* Bytes of device workspace for sparse_attn_bwd (n_anchor = 0) or sparse_attn_bwd_repeat
+ * (n_anchor = calib_anchor_count(...)); host computation.  -1 for invalid sizes. */
+int64_t sparse_attn_bwd_workspace(int H, int N, int D, int block, int n_anchor, uint32_t flags);
+
+/* Gradients of sparse_attn_fwd, recomputing the probabilities from the saved LSE:
+ *   P_rc = exp(scale * q_r.k_c - LSE_r) on the kept blocks, delta_r = sum_d dout_rd o_rd,
+ *   dS_rc = P_rc (dout_r.v_c - delta_r),
+ *   dq_r = scale sum_c dS_rc k_c,  dk_c = scale sum_r dS_rc q_r,  dv_c = sum_r P_rc dout_r.
+ *   q, k, v    : bf16 [H, N, D], as given to sparse_attn_fwd with the same scale and list.
+ *   o, lse     : its outputs; lse fp32 [H, N] (lse_opt of that call) is required.
+ *   dout       : gradient of o, [H, N, D] in o's type.
+ *   dq, dk, dv : bf16 [H, N, D] (fp32 with CALIB_ATTN_GRAD_F32), overwritten; every element is
+ *                written (0 where a query block keeps nothing or a key block is kept by none).
+ *   list       : the forward call's list; a work order, if given, must hold H*nq entries.
+ *   list_t     : the same list by key block (calib_transpose_csr), H, nk, nq, block; a work
+ *                order, if given, must hold H*nk entries.
+ *   flags      : CALIB_ATTN_OUT_F32 as in the forward call (o and dout are then fp32),
+ *                CALIB_ATTN_GRAD_F32.
+ *   workspace  : 16-byte aligned, sparse_attn_bwd_workspace(H, N, D, list->block, 0, flags)
+ *                bytes; its contents need not be set, are not kept for a later call, and one
+ *                buffer serves one call at a time.
+ * Outputs must not overlap inputs, the workspace or each other.  Pointers are 16-byte aligned
+ * (lse: 4).  Arithmetic: all products on the tensor cores with fp32 accumulation; P, dS and an
+ * fp32 dout enter them as bf16.  Sums are taken in a fixed order (no atomics): the same call
+ * gives the same bits.  No gradient flows through the LSE. */
+calib_status sparse_attn_bwd(const void* q, const void* k, const void* v, const void* o,
+                             const void* dout, const float* lse, void* dq, void* dk, void* dv,
+                             int H, int N, int D, float scale, const calib_block_list* list,
+                             const calib_block_list* list_t, uint32_t flags, void* workspace,
+                             int64_t workspace_bytes, void* stream);
+
+/* Gradients of sparse_attn_fwd_repeat.  In a repeat head every token's output is its
+ * anchor's, so the gradients of the tokens that take an anchor's output add up at the anchor;
+ * dq of the other (non-anchor) video tokens is 0.  list rows of a repeat head are in anchor
+ * block space, and list_t of that head holds those rows' indices.  Repeat arguments as
+ * sparse_attn_fwd_repeat; workspace of sparse_attn_bwd_workspace(H, N, D, list->block,
+ * calib_anchor_count(F, Hl, Wl, n_text, stride), flags) bytes; everything else as
+ * sparse_attn_bwd.  The summed dout enters the products as bf16. */
+calib_status sparse_attn_bwd_repeat(const void* q, const void* k, const void* v, const void* o,
+                                    const void* dout, const float* lse, void* dq, void* dk,
+                                    void* dv, int H, int D, int F, int Hl, int Wl, int n_text,
+                                    int stride, const uint8_t* head_repeat, float scale,
+                                    const calib_block_list* list, const calib_block_list* list_t,
+                                    uint32_t flags, void* workspace, int64_t workspace_bytes,
+                                    void* stream);
+
+/* A paged key/value cache in 8 bits, shared by the two calls below.
+ *   k_cache, v_cache : e4m3 [pages, Hkv, B, D], 16-byte aligned; B in {64, 128}, D in {64, 128}.
+ *   k_scale, v_scale : fp32 [pages, Hkv]: a value is its e4m3 number times the scale of its
+ *                      block (page) and head.
+ *   block_table      : int32 [S, max_blocks]; block b of sequence s is page block_table[s, b].
+ *                      Only the first ceil(lengths[s] / B) entries of a row are read.
+ *   lengths          : int32 [S], tokens of each sequence, the new ones included; 0 is a free
+ *                      slot of the batch.
+ *   new_lens         : int32 [S] or NULL (M each): how many of the call's M token slots a
+ *                      sequence uses; slot m < new_lens[s] is position lengths[s] -
+ *                      new_lens[s] + m.  The slots behind are padding.
+ * A length outside [0, max_blocks * B] or a count outside [0, min(M, lengths[s])] leaves that
+ * sequence out, a page outside [0, pages) that block; both are reported (calib_device_check).
+ * pages * Hkv * B and max_blocks * B are below 2^31 (CALIB_ERR_UNSUPPORTED beyond). */
+
+/* Writes new tokens into the cache.
+ *   k_new, v_new : bf16 [S, Hkv, M, D]; slots behind new_lens[s] are not read.
+ * A touched block's scale becomes max(largest finite magnitude of its new tokens, 2^-100) / 448,
+ * or stays as it was if it held earlier tokens and its scale was larger; earlier tokens are
+ * rounded again when their block's scale grows.  Values are rounded to the nearest e4m3 (ties to
+ * even), infinities become +-448 * scale, NaN stays NaN.  Bytes at and behind a sequence's end are
+ * left as they were.  Writing the same tokens at the same lengths again changes nothing.  A page
+ * must not be written for two sequences in one call. */
+calib_status calib_cache_write(const void* k_new, const void* v_new, void* k_cache, void* v_cache,
+                               float* k_scale, float* v_scale, const int32_t* block_table,
+                               const int32_t* lengths, const int32_t* new_lens, int S, int Hkv,
+                               int M, int D, int block, int max_blocks, int64_t pages,
+                               void* stream);
+
+/* Bytes of device workspace for sparse_attn_cached (0: none is needed); host computation.
+ * -1 for invalid sizes. */
+int64_t sparse_attn_cached_workspace(int S, int Hq, int Hkv, int M, int D, int block,
+                                     int max_blocks);
+
+/* Attention of M query tokens of each of S sequences over its cached keys and values.
+ *   q, o       : bf16 [S, Hq, M, D] (o fp32 with CALIB_ATTN_OUT_F32), 16-byte aligned; query
+ *                head h reads K/V head h / (Hq / Hkv).
+ *   lse_opt    : NULL or fp32 [S, Hq, M], natural-log LSE.
+ *   list       : NULL (every block), or a skip list with H = Hkv, nq = S, nk = max_blocks and
+ *                the cache's block size: row (h, s) holds the blocks of sequence s that the
+ *                query heads of K/V head h attend to.  Blocks past the sequence's end are
+ *                ignored; `work` is not used.
+ *   flags      : CALIB_ATTN_OUT_F32; CALIB_ATTN_CAUSAL: slot m sees the keys at or before its
+ *                position (the queries are the sequence's last new_lens[s] tokens).  Without it
+ *                every used slot sees all lengths[s] keys.
+ *   workspace  : 16-byte aligned, sparse_attn_cached_workspace(...) bytes, NULL if that is 0; its
+ *                contents need not be set, and one buffer serves one call at a time.
+ * Rows without keys (padding slots, free batch slots, nothing kept) write O = 0, LSE = -inf.
+ * Cache bytes behind a sequence's end may hold anything; values before it are expected finite (a
+ * NaN or scale that is not finite there can reach every row of its sequence and head).
+ * Arithmetic: e4m3 values enter the products exactly, q and P as fp16 (q scaled by a power of two
+ * per row), with fp32 accumulation; sums in a fixed order. */
+calib_status sparse_attn_cached(const void* q, const void* k_cache, const void* v_cache,
+                                const float* k_scale, const float* v_scale,
+                                const int32_t* block_table, const int32_t* lengths,
+                                const int32_t* new_lens, void* o, float* lse_opt, int S, int Hq,
+                                int Hkv, int M, int D, int block, int max_blocks, int64_t pages,
+                                float scale, const calib_block_list* list, uint32_t flags,
+                                void* workspace, int64_t workspace_bytes, void* stream);
 
 /* Checks a skip list held in HOST memory (copied back from the device by the caller) before
  * it is given to the attention calls, which trust the list's structure: row_ptr[0] == 0;

@@ -26,4 +26,5 @@ from .calibatt_ref import (  # noqa: F401
     aggregate_masks, mask_to_csr, csr_to_intervals, intervals_to_csr, build_schedule, anchor_rows,
     anchor_index_of_token, anchor_token, repeat_similarity, repeat_flags,
     sparse_attention, sparse_attention_repeat, ceil_log2,
+    sparse_attention_grads, sparse_attention_repeat_grads, transpose_csr, cached_attention, cache_scales,
 )

@@ -426,3 +426,113 @@ def sparse_attention_repeat(q, k, v, scale: float, block: int, mask: np.ndarray,
         O[h] = Oa[0][amap]
         L[h] = La[0][amap]
     return O, L
+
+
+# ------------------------------------------------------------------------------------
+# gradients of the sparse attention, and attention over a cache in 8 bits
+# ------------------------------------------------------------------------------------
+
+def sparse_attention_grads(q, k, v, o, do, lse, scale: float, block: int, mask: np.ndarray):
+    """dq, dk, dv of sum(o * do) for o = sparse_attention(q, k, v), from the saved o and LSE.
+
+    With P_rc = exp(S_rc - LSE_r) on the kept blocks (0 elsewhere), o = P v gives
+    dv = P^T do and dP = do v^T; the softmax's Jacobian is diag(P) - P P^T, so
+    dS = P * (dP - delta) with delta_r = sum_c P_rc dP_rc = do_r . o_r; and S = scale q k^T
+    gives dq = scale dS k, dk = scale dS^T q.
+    q, o, do [H, Nq, D]; k, v [H, N, D]; lse [H, Nq]; mask [H, >=nq, nk]."""
+    q, k, v, o, do, lse = (np.asarray(x, np.float64) for x in (q, k, v, o, do, lse))
+    dq, dk, dv = np.zeros_like(q), np.zeros_like(k), np.zeros_like(v)
+    Nq, N = q.shape[1], k.shape[1]
+    nq = -(-Nq // block)
+    for h in range(q.shape[0]):
+        for i in range(nq):
+            r = slice(i * block, min((i + 1) * block, Nq))
+            for j in np.nonzero(mask[h, i])[0]:
+                c = slice(j * block, min((j + 1) * block, N))
+                P = np.exp(logits(q[h, r], k[h, c], scale) - lse[h, r, None])
+                dS = P * (do[h, r] @ v[h, c].T - (do[h, r] * o[h, r]).sum(1)[:, None])
+                dq[h, r] += scale * dS @ k[h, c]
+                dk[h, c] += scale * dS.T @ q[h, r]
+                dv[h, c] += P.T @ do[h, r]
+    return dq, dk, dv
+
+
+def sparse_attention_repeat_grads(q, k, v, o, do, lse, scale: float, block: int, mask: np.ndarray,
+                                  head_repeat, F: int, Hl: int, Wl: int, n_text: int, stride: int):
+    """dq, dk, dv of sparse_attention_repeat.  A flagged head's output is its anchors' output
+    copied to their tokens, so the anchors receive the sum of their tokens' gradients, and q of
+    the other tokens enters nowhere."""
+    N = q.shape[1]
+    A = anchor_rows(F, Hl, Wl, n_text, stride)
+    amap = np.array([anchor_index_of_token(t, F, Hl, Wl, n_text, stride) for t in range(N)])
+    outs = []
+    for h in range(q.shape[0]):
+        one = [np.asarray(x[h:h + 1], np.float64) for x in (q, k, v, o, do, lse)]
+        if head_repeat[h]:
+            qh, kh, vh, oh, doh, lh = one
+            da = np.zeros((1, len(A), q.shape[2]))
+            np.add.at(da[0], amap, doh[0])
+            dqa, dkh, dvh = sparse_attention_grads(qh[:, A], kh, vh, oh[:, A], da, lh[:, A], scale, block, mask[h:h + 1])
+            dqh = np.zeros_like(qh)
+            dqh[:, A] = dqa
+            outs.append((dqh, dkh, dvh))
+        else:
+            outs.append(sparse_attention_grads(*one, scale, block, mask[h:h + 1]))
+    return tuple(np.concatenate(x) for x in zip(*outs))
+
+
+def transpose_csr(row_ptr: np.ndarray, col_idx: np.ndarray, H: int, nq: int, nk: int):
+    """The skip list by key block: row h*nk + j holds the ascending query blocks i whose row
+    h*nq + i holds j."""
+    ptr, col = [0], []
+    for h in range(H):
+        for j in range(nk):
+            for i in range(nq):
+                r = h * nq + i
+                if j in col_idx[row_ptr[r]:row_ptr[r + 1]]:
+                    col.append(i)
+            ptr.append(len(col))
+    return np.array(ptr, np.int32), np.array(col, np.int16)
+
+
+def cached_attention(q, k_cache, v_cache, k_scale, v_scale, table, lengths, new_lens, scale: float,
+                     causal: bool, mask=None):
+    """Attention of the last new_lens[s] tokens of each sequence over its cached keys and values.
+
+    q [S, Hq, M, D]; caches (numbers, not bytes) [pages, Hkv, B, D] with scales [pages, Hkv]; block b of
+    sequence s is page table[s, b].  Slot m < new_lens[s] stands at position lengths[s] - new_lens[s] + m
+    and sees the keys at or before it (causal) or all lengths[s]; mask [Hkv, S, >=blocks] restricts it to
+    kept blocks.  Query head h reads K/V head h // (Hq // Hkv).  Rows without keys: O = 0, LSE = -inf.
+    Returns (O, LSE, sum_c P_c |v_c|)."""
+    S, Hq, M, D = q.shape
+    Hkv, B = k_cache.shape[1:3]
+    O, L, A = np.zeros(q.shape), np.full((S, Hq, M), -np.inf), np.zeros(q.shape)
+    for s in range(S):
+        n = int(lengths[s])
+        pages = table[s, : -(-n // B)]
+        for h in range(Hq):
+            g = h // (Hq // Hkv)
+            K = (np.asarray(k_cache[pages, g], np.float64) * np.asarray(k_scale[pages, g], np.float64)[:, None, None]).reshape(-1, D)[:n]
+            V = (np.asarray(v_cache[pages, g], np.float64) * np.asarray(v_scale[pages, g], np.float64)[:, None, None]).reshape(-1, D)[:n]
+            for m in range(int(new_lens[s])):
+                allowed = np.arange(n) < (n - int(new_lens[s]) + m + 1 if causal else n)
+                if mask is not None:
+                    allowed &= np.repeat(np.asarray(mask[g, s], bool), B)[:n]
+                if not allowed.any():
+                    continue
+                x = scale * K[allowed] @ np.asarray(q[s, h, m], np.float64)
+                w = np.exp(x - x.max())
+                O[s, h, m] = w @ V[allowed] / w.sum()
+                A[s, h, m] = w @ np.abs(V[allowed]) / w.sum()
+                L[s, h, m] = x.max() + np.log(w.sum())
+    return O, L, A
+
+
+def cache_scales(k_new, held, lo: int, hi: int):
+    """Scale of a block whose tokens [lo, hi) are new (k_new [.., hi - lo, D]) and whose earlier
+    tokens have the scale `held`: that of the largest finite new magnitude, which a block with
+    earlier tokens only raises."""
+    x = np.abs(np.asarray(k_new, np.float64))
+    amax = np.where(np.isfinite(x), x, 0.0).max(initial=0.0)
+    scale = max(amax, 2.0 ** -100) / 448.0
+    return max(scale, held) if lo > 0 else scale

@@ -1,0 +1,456 @@
+"""Gradients of block-sparse attention and the transposed skip list.
+
+CPU: the oracle's gradients against torch's autograd in 64 bits and against differences, the
+transposed list's definition, and the refusals that need no device.  GPU (marked): the kernels
+against the oracle.
+
+Tolerances.  With P and dS rounded to bf16 before their products (each off by at most 2^-8 of its
+value), fp32 sums, and the result rounded once:
+  |err dv| <= (u + e) |P|^T |do|                       + u_out |dv|
+  |err dq| <= scale ((u + e) |dS| + |P| d) |k|         + u_out |dq|     (dk likewise, transposed)
+where u = 2^-8, e = the relative error of P = exp(S - LSE) plus the sums' (D + 8) 2^-24 max|scale q||k|
++ N 2^-24 + 2^-20 (the exponential), d = (D + 8) 2^-24 (|do||v|^T + sum|do||o|) is the error of dP - delta,
+and u_out = 2^-8 for bf16 results, 2^-24 for fp32 ones.  An fp32 dout, or a repeat head's summed one,
+is itself rounded to bf16: then do carries another u (u |P|^T|do| in dv, u |do||v|^T in d).
+That bound adds every rounding up as if all were largest and of one sign; the roundings' expected
+squares (a value off by at most u |x| has a mean square of at most u^2 x^2 / 3 over the positions in a
+step) give the second check, ||err|| <= 2 sqrt(expected), which a wrong term in a few hundred fails.
+"""
+import ctypes
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from calibrated_block_sparse_calib_b200 import ops
+from conftest import to64
+
+U16, U32 = 2.0 ** -8, 2.0 ** -24
+
+
+def _mask(rng, H, nq, nk, p, holes=True):
+    m = (rng.random((H, nq, nk)) < p).astype(np.uint8)
+    if nq > 1:
+        m[:, np.arange(nq), np.minimum(np.arange(nq), nk - 1)] = 1
+        if holes and nk > 2:
+            m[0, nq // 2] = 0                                     # a query block that keeps nothing
+            m[-1, :, nk // 2] = 0                                 # a key block that none keeps
+    else:
+        m[:] = 1
+    return m
+
+
+# ------------------------------------------------------------------------------------
+# the oracle (CPU)
+# ------------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("N,B", [(1, 64), (65, 64), (200, 64), (130, 128)])
+def test_oracle_grads_against_autograd(N, B):
+    rng = np.random.default_rng(N)
+    H, D, scale = 2, 16, 0.3
+    q, k, v, do = (rng.standard_normal((H, N, D)) for _ in range(4))
+    nb = -(-N // B)
+    mask = _mask(rng, H, nb, nb, 0.5)
+    o, lse = oracle.sparse_attention(q, k, v, scale, B, mask)
+    got = oracle.sparse_attention_grads(q, k, v, o, do, lse, scale, B, mask)
+    t = [torch.from_numpy(x).requires_grad_() for x in (q, k, v)]
+    keep = torch.from_numpy(np.kron(mask, np.ones((1, B, B)))[:, :N, :N] > 0)
+    s = (scale * t[0] @ t[1].transpose(1, 2)).masked_fill(~keep, -1e300)
+    p = torch.softmax(s, -1) * keep
+    ref = torch.autograd.grad((p @ t[2] * torch.from_numpy(do)).sum(), t)
+    for x, y in zip(got, ref):
+        np.testing.assert_allclose(x, y.numpy(), rtol=1e-10, atol=1e-12)
+
+
+def test_oracle_repeat_grads_against_differences():
+    rng = np.random.default_rng(3)
+    F, Hl, Wl, n_text, stride, B, D, scale = 2, 5, 3, 2, 2, 64, 4, 0.4
+    N = F * Hl * Wl + n_text
+    q, k, v, do = (rng.standard_normal((2, N, D)) for _ in range(4))
+    mask = np.ones((2, 1, 1), np.uint8)
+    rep = [True, False]
+    fwd = lambda *x: oracle.sparse_attention_repeat(*x, scale, B, mask, rep, F, Hl, Wl, n_text, stride)
+    o, lse = fwd(q, k, v)
+    got = oracle.sparse_attention_repeat_grads(q, k, v, o, do, lse, scale, B, mask, rep, F, Hl, Wl, n_text, stride)
+    for which in range(3):
+        for _ in range(12):
+            at = tuple(rng.integers(0, n) for n in q.shape)
+            eps, vals = 1e-5, []
+            for sign in (1, -1):
+                x = [q.copy(), k.copy(), v.copy()]
+                x[which][at] += sign * eps
+                vals.append((fwd(*x)[0] * do).sum())
+            # central differences: truncation eps^2, cancellation 1e-16 / eps
+            np.testing.assert_allclose(got[which][at], (vals[0] - vals[1]) / (2 * eps), rtol=1e-6, atol=1e-8)
+
+
+def test_oracle_transpose_is_the_transposed_mask():
+    rng = np.random.default_rng(0)
+    m = (rng.random((3, 7, 11)) < 0.4).astype(np.uint8)
+    got = oracle.transpose_csr(*oracle.mask_to_csr(m), 3, 7, 11)
+    ref = oracle.mask_to_csr(np.ascontiguousarray(m.transpose(0, 2, 1)))
+    np.testing.assert_array_equal(got[0], ref[0])
+    np.testing.assert_array_equal(got[1], ref[1])
+
+
+# ------------------------------------------------------------------------------------
+# refusals (CPU: decided before any device work)
+# ------------------------------------------------------------------------------------
+
+def test_refusals_before_device_work():
+    L, null, fake = ops.lib(), ctypes.c_void_p(0), ctypes.c_void_p(256)
+    bl = ops._BlockListC(1, 2, 2, 64, 256, 256, 0, 0)
+    big = 1 << 40
+
+    def bwd(q=fake, lse=fake, dq=fake, H=1, N=128, D=64, scale=0.1, lst=bl, lst_t=bl, flags=0, space=fake, size=big):
+        return L.sparse_attn_bwd(q, fake, fake, fake, fake, lse, dq, fake, fake, H, N, D, scale, ctypes.byref(lst),
+                                 ctypes.byref(lst_t), flags, space, size, null)
+
+    bad, unsupported = ops.CALIB_ERR_INVALID, ops.CALIB_ERR_UNSUPPORTED
+    assert bwd(q=null) == bwd(lse=null) == bwd(dq=null) == bwd(space=null) == bad
+    assert bwd(dq=ctypes.c_void_p(264)) == bwd(space=ctypes.c_void_p(264)) == bad         # alignment
+    assert bwd(lse=ctypes.c_void_p(258)) == bad
+    assert bwd(scale=0.0) == bwd(scale=float("nan")) == bwd(flags=4) == bwd(N=200) == bad
+    assert bwd(D=96) == unsupported
+    if not torch.cuda.is_available():
+        return        # what follows is decided after the device check, which fails without a device
+    assert bwd(size=ops.lib().sparse_attn_bwd_workspace(1, 128, 64, 64, 0, 0) - 1) == bad
+    assert bwd(lst_t=ops._BlockListC(1, 2, 3, 64, 256, 256, 0, 0)) == bad
+    assert bwd(lst=ops._BlockListC(1, 2, 2, 64, 256, 256, 256, 1)) == bad                # a partial work order
+
+
+def test_refusals_of_the_other_calls():
+    L, null, fake = ops.lib(), ctypes.c_void_p(0), ctypes.c_void_p(256)
+    bad = ops.CALIB_ERR_INVALID
+    assert L.calib_transpose_csr(null, fake, 1, 1, 1, fake, fake, null) == bad
+    assert L.calib_transpose_csr(fake, fake, 0, 1, 1, fake, fake, null) == bad
+    assert L.calib_transpose_csr(fake, fake, 1, 32768, 1, fake, fake, null) == bad
+    rep = (ctypes.c_uint8 * 1)(1)
+    bl = ops._BlockListC(1, 2, 2, 64, 256, 256, 0, 0)
+    args = [fake] * 9
+    assert L.sparse_attn_bwd_repeat(*args, 1, 64, 1, 2, 64, 0, 0, ctypes.cast(rep, ctypes.c_void_p), 0.1,
+                                    ctypes.byref(bl), ctypes.byref(bl), 0, fake, 1 << 40, null) == bad      # stride 0
+    assert L.sparse_attn_bwd_repeat(*args, 1, 64, 1, 2, 64, 0, 1, null, 0.1, ctypes.byref(bl), ctypes.byref(bl), 0,
+                                    fake, 1 << 40, null) == bad
+    assert L.sparse_attn_bwd_workspace(0, 1, 64, 64, 0, 0) == L.sparse_attn_bwd_workspace(1, 1, 96, 64, 0, 0) == -1
+    assert L.sparse_attn_bwd_workspace(1, 10, 64, 64, 11, 0) == L.sparse_attn_bwd_workspace(1, 1, 64, 64, 0, 4) == -1
+    assert L.sparse_attn_bwd_workspace(2, 100, 64, 64, 0, 0) == 2 * 128 * 8
+    assert L.sparse_attn_bwd_workspace(2, 100, 64, 64, 50, 0) == 2 * 128 * 8 + 2 * (2 * 50 * 64 * 2)
+
+
+def test_host_tensors_are_refused():
+    q = torch.zeros(1, 64, 64, dtype=torch.bfloat16)
+    bl = ops.BlockList(1, 1, 1, 64, torch.zeros(2, dtype=torch.int32), torch.zeros(1, dtype=torch.int16))
+    with pytest.raises(TypeError, match="CUDA tensor"):
+        ops.sparse_attn_bwd(q, q, q, q, q, torch.zeros(1, 64), bl)
+    with pytest.raises(TypeError, match="CUDA tensor"):
+        ops.transpose_csr(bl.row_ptr, bl.col_idx, 1, 1, 1)
+    with pytest.raises(TypeError, match="CUDA tensor"):
+        bl.transpose()
+    with pytest.raises(ValueError, match="F\\*Hl\\*Wl"):
+        ops.sparse_attn_bwd_repeat(q, q, q, q, q, torch.zeros(1, 64), bl, [True], 1, 1, 63, 0, 1)
+
+
+# ------------------------------------------------------------------------------------
+# the transposed list (GPU): exact
+# ------------------------------------------------------------------------------------
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("H,nq,nk,p", [(1, 1, 1, 1.0), (2, 8, 8, 0.5), (3, 37, 53, 0.3), (2, 31, 33, 1.0),
+                                       (1, 64, 32, 0.0), (40, 158, 591, 0.2), (2, 1500, 40, 0.3), (1, 7, 4000, 0.05)])
+def test_transpose_exact(H, nq, nk, p):
+    rng = np.random.default_rng(H * nq + nk)
+    m = (rng.random((H, nq, nk)) < p).astype(np.uint8)
+    ref_ptr, ref_col = oracle.mask_to_csr(np.ascontiguousarray(m.transpose(0, 2, 1)))
+    rp, ci = (torch.from_numpy(x).cuda() for x in oracle.mask_to_csr(m))
+    tp, tc = ops.transpose_csr(rp, ci, H, nq, nk)
+    np.testing.assert_array_equal(tp.cpu().numpy(), ref_ptr)
+    np.testing.assert_array_equal(tc.cpu().numpy(), ref_col)
+    ops.device_check()
+    bl = ops.BlockList(H, nq, nk, 64, rp, ci).transpose().validate()
+    np.testing.assert_array_equal(bl.work.cpu().numpy(), oracle.build_schedule(ref_ptr, H, nk))
+    back = bl.transpose(schedule=False)
+    np.testing.assert_array_equal(back.row_ptr.cpu().numpy(), rp.cpu().numpy())
+    np.testing.assert_array_equal(back.col_idx.cpu().numpy(), ci.cpu().numpy())
+
+
+@pytest.mark.gpu
+def test_transpose_of_the_longest_rows_and_of_a_capacity_sized_list():
+    """32767 query blocks (the most), and a column array with room behind the last entry, which is left
+    as it was."""
+    rng = np.random.default_rng(1)
+    m = (rng.random((1, 32767, 33)) < 0.1).astype(np.uint8)
+    bl = ops.BlockList.from_mask(torch.from_numpy(m).cuda(), 64, schedule=False)
+    n = int(bl.row_ptr[-1])
+    tp, tc = ops.transpose_csr(bl.row_ptr, bl.col_idx, 1, 32767, 33)
+    ref_ptr, ref_col = oracle.mask_to_csr(np.ascontiguousarray(m.transpose(0, 2, 1)))
+    np.testing.assert_array_equal(tp.cpu().numpy(), ref_ptr)
+    np.testing.assert_array_equal(tc[:n].cpu().numpy(), ref_col)
+    ops.device_check()
+
+
+# ------------------------------------------------------------------------------------
+# gradients (GPU)
+# ------------------------------------------------------------------------------------
+
+def _bounds(q, k, v, o, do, lse, scale, B, mask, u_do):
+    """Oracle gradients of one head ([N, D] each), their largest and their expected-square errors before the
+    output's rounding."""
+    Nq, N, D = len(q), len(k), q.shape[1]
+    keep = np.kron(mask, np.ones((B, B)))[:Nq, :N] > 0
+    with np.errstate(over="ignore", invalid="ignore"):
+        P = np.where(keep, np.exp(scale * q @ k.T - lse[:, None]), 0.0)
+    delta = (do * o).sum(1)
+    dP = do @ v.T
+    dS = P * (dP - delta[:, None])
+    size = scale * np.abs(q) @ np.abs(k).T
+    e = (D + 8) * U32 * size.max(initial=0.0) + max(N, Nq) * U32 + 2.0 ** -20
+    d32 = (D + 8) * U32 * (np.abs(do) @ np.abs(v).T + (np.abs(do) * np.abs(o)).sum(1)[:, None])
+    d = d32 + u_do * (np.abs(do) @ np.abs(v).T)
+    aS = (U16 + e) * np.abs(dS) + P * d
+    most = (scale * aS @ np.abs(k), scale * aS.T @ np.abs(q), (U16 + e + u_do) * P.T @ np.abs(do))
+    # d32 counts too: where dP - delta cancels (one key: P = 1 and o = v, dS is 0 exactly) it is all there is
+    sq = (U16 ** 2 / 3 + e ** 2) * dS ** 2 + (P * d32) ** 2 + P ** 2 * (u_do ** 2 / 3 * (do ** 2 @ (v ** 2).T))
+    mean = (scale ** 2 * sq @ k ** 2, scale ** 2 * sq.T @ q ** 2,
+            ((U16 ** 2 + u_do ** 2) / 3 + e ** 2) * (P ** 2).T @ do ** 2)
+    return (scale * dS @ k, scale * dS.T @ q, P.T @ do), most, mean
+
+
+def _check(got, ref, most, mean, name):
+    g, u = to64(got), U16 if got.dtype == torch.bfloat16 else U32
+    err = np.abs(g - ref)
+    assert np.isfinite(g).all(), name
+    # 2^-126: results below the smallest normal number are rounded to multiples of its last place
+    over = err - (most * (1 + u) + u * np.abs(ref) + 2.0 ** -126)
+    assert over.max(initial=-1.0) <= 0, (name, float(err.max()), float(over.max()))
+    expected = mean + u ** 2 / 3 * ref ** 2
+    assert math.sqrt((err ** 2).sum()) <= 2 * math.sqrt(expected.sum()) + 1e-30, \
+        (name, math.sqrt((err ** 2).sum()), math.sqrt(expected.sum()))
+
+
+def _inputs(H, N, D, seed, io=torch.bfloat16, spread=1.0):
+    g = torch.Generator().manual_seed(seed)
+    q, k, v, do = (torch.randn(H, N, D, generator=g) for _ in range(4))
+    return [x.to(torch.bfloat16).cuda() for x in (q * spread, k * spread, v)] + [do.to(torch.bfloat16).to(io).cuda()
+                                                                                if io == torch.bfloat16 else do.cuda()]
+
+
+def _compare(q, k, v, o, do, lse, mask, B, grads, scale=None):
+    q, k, v, o, dd, lse = (to64(x) for x in (q, k, v, o, do, lse))
+    u_do = U16 if do.dtype == torch.float32 else 0.0
+    scale = q.shape[2] ** -0.5 if scale is None else scale
+    for h in range(q.shape[0]):
+        ref, most, mean = _bounds(q[h], k[h], v[h], o[h], dd[h], lse[h], scale, B, mask[h], u_do)
+        for x, r, a, b, n in zip(grads, ref, most, mean, ("dq", "dk", "dv")):
+            _check(x[h], r, a, b, f"{n} head {h}")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("H,N,D,B,p", [
+    (1, 1, 64, 64, 1.0), (2, 1, 128, 128, 1.0), (1, 2, 128, 64, 1.0), (2, 63, 64, 64, 1.0), (1, 64, 128, 64, 1.0),
+    (2, 65, 64, 64, 0.7), (3, 127, 128, 128, 1.0), (2, 128, 64, 128, 1.0), (2, 129, 128, 128, 0.7),
+    (2, 200, 128, 64, 0.5), (3, 500, 64, 64, 0.4), (2, 513, 128, 128, 0.5), (2, 700, 64, 128, 0.6),
+    (5, 1000, 128, 64, 0.3), (2, 1300, 128, 128, 0.4), (1, 900, 128, 128, 1.0)])
+def test_grads(H, N, D, B, p):
+    q, k, v, do = _inputs(H, N, D, N + D)
+    nb = ops.nblocks(N, B)
+    mask = _mask(np.random.default_rng(N), H, nb, nb, p)
+    bl = ops.BlockList.from_mask(torch.from_numpy(mask).cuda(), B)
+    o, lse = ops.sparse_attn_fwd(q, k, v, bl, return_lse=True)
+    grads = ops.sparse_attn_bwd(q, k, v, o, do, lse, bl, bl.transpose())
+    ops.device_check()
+    assert all(x.dtype == torch.bfloat16 for x in grads)
+    _compare(q, k, v, o, do, lse, mask, B, grads)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("D,B", [(64, 64), (128, 128), (64, 128), (128, 64)])
+def test_grads_fp32_in_and_out_and_unordered_lists(D, B):
+    H, N = 3, 450
+    q, k, v, do = _inputs(H, N, D, D + B, io=torch.float32)
+    nb = ops.nblocks(N, B)
+    mask = _mask(np.random.default_rng(B), H, nb, nb, 0.5)
+    bl = ops.BlockList.from_mask(torch.from_numpy(mask).cuda(), B, schedule=False)
+    o, lse = ops.sparse_attn_fwd(q, k, v, bl, return_lse=True, out_dtype=torch.float32, scale=0.2)
+    grads = ops.sparse_attn_bwd(q, k, v, o, do, lse, bl, bl.transpose(schedule=False), scale=0.2,
+                                grad_dtype=torch.float32)
+    ops.device_check()
+    assert all(x.dtype == torch.float32 for x in grads)
+    _compare(q, k, v, o, do, lse, mask, B, grads, scale=0.2)
+
+
+@pytest.mark.gpu
+def test_grads_large_logits():
+    """Logits of several hundred: P is 0 or near 1, the LSE far from 0 (and 0 outside the sequence's end)."""
+    H, N, D, B = 2, 300, 64, 128
+    q, k, v, do = _inputs(H, N, D, 9, spread=6.0)
+    mask = np.ones((H, 3, 3), np.uint8)
+    bl = ops.BlockList.from_mask(torch.from_numpy(mask).cuda(), B)
+    for shift in (0.0, -12.0):                # a common key component moves every logit of a row by a constant
+        kk = (k.float() + shift).to(torch.bfloat16)
+        qq = (q.float() + 8.0).to(torch.bfloat16)
+        o, lse = ops.sparse_attn_fwd(qq, kk, v, bl, return_lse=True)
+        _compare(qq, kk, v, o, do, lse, mask, B, ops.sparse_attn_bwd(qq, kk, v, o, do, lse, bl))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("B", [64, 128])
+def test_blocks_nobody_keeps_do_not_reach_the_rest(B):
+    """NaN in the keys and values of a block that no query keeps, and in the queries and output gradients of
+    a block that keeps nothing: those blocks' gradients are 0 and no other is touched."""
+    H, N, D = 2, 4 * B + 17, 128
+    q, k, v, do = _inputs(H, N, D, 5)
+    mask = np.ones((H, 5, 5), np.uint8)
+    mask[:, :, 1] = 0
+    mask[:, 2] = 0
+    bl = ops.BlockList.from_mask(torch.from_numpy(mask).cuda(), B)
+    kc, qr = slice(B, 2 * B), slice(2 * B, 3 * B)
+    for x in (k, v):
+        x[:, kc] = math.nan
+    for x in (q, do):
+        x[:, qr] = math.nan
+    o, lse = ops.sparse_attn_fwd(q, k, v, bl, return_lse=True)
+    grads = ops.sparse_attn_bwd(q, k, v, o, do, lse, bl)
+    assert not grads[0][:, qr].any() and not grads[1][:, kc].any() and not grads[2][:, kc].any()
+    for x in (k, v):
+        x[:, kc] = 0
+    for x in (q, do):
+        x[:, qr] = 0
+    _compare(q, k, v, o, do, lse, mask, B, grads)
+
+
+@pytest.mark.gpu
+def test_empty_list_gives_zeros():
+    H, N, D, B = 2, 150, 64, 64
+    q, k, v, do = _inputs(H, N, D, 1)
+    bl = ops.BlockList.from_mask(torch.zeros(H, 3, 3, dtype=torch.uint8, device="cuda"), B)
+    o, lse = ops.sparse_attn_fwd(q, k, v, bl, return_lse=True)
+    grads = [torch.full((H, N, D), 7.0, dtype=torch.bfloat16, device="cuda") for _ in range(3)]
+    out = ops.sparse_attn_bwd(q, k, v, o, do, lse, bl, dq=grads[0], dk=grads[1], dv=grads[2])
+    assert all(a is b and not a.any() for a, b in zip(out, grads))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("F,Hl,Wl,n_text,stride,D,B,io", [
+    (2, 8, 16, 0, 2, 64, 64, torch.bfloat16), (3, 7, 11, 5, 3, 128, 64, torch.bfloat16),
+    (2, 9, 13, 70, 4, 128, 128, torch.bfloat16), (1, 5, 3, 1, 1, 64, 128, torch.bfloat16),
+    (2, 6, 10, 3, 9, 64, 64, torch.float32)])
+def test_repeat_grads(F, Hl, Wl, n_text, stride, D, B, io):
+    H, N = 3, F * Hl * Wl + n_text
+    rep = [True, False, True]
+    q, k, v, do = _inputs(H, N, D, N, io=io)
+    nb = ops.nblocks(N, B)
+    A = oracle.anchor_rows(F, Hl, Wl, n_text, stride)
+    amap = np.array([oracle.anchor_index_of_token(t, F, Hl, Wl, n_text, stride) for t in range(N)])
+    mask = _mask(np.random.default_rng(N), H, nb, nb, 0.6, holes=False)
+    nqa = -(-len(A) // B)
+    mask[1, 0, -1] = 1
+    bl = ops.BlockList.from_mask(torch.from_numpy(mask).cuda(), B)      # rows past the anchors are ignored
+    o, lse = ops.sparse_attn_fwd_repeat(q, k, v, bl, rep, F, Hl, Wl, n_text, stride, return_lse=True, out_dtype=io)
+    grads = ops.sparse_attn_bwd_repeat(q, k, v, o, do, lse, bl, rep, F, Hl, Wl, n_text, stride)
+    ops.device_check()
+    full = oracle.sparse_attention_repeat_grads(*(to64(x) for x in (q, k, v, o, do, lse)), D ** -0.5, B,
+                                                np.where(np.arange(nb)[None, :, None] < np.array([nqa, nb, nqa])[:, None, None], mask, 0),
+                                                rep, F, Hl, Wl, n_text, stride)
+    q6, k6, v6, o6, d6, l6 = (to64(x) for x in (q, k, v, o, do, lse))
+    for h in range(H):
+        if rep[h]:
+            da = np.zeros((len(A), D))
+            np.add.at(da, amap, d6[h])
+            ref, most, mean = _bounds(q6[h][A], k6[h], v6[h], o6[h][A], da, l6[h][A], D ** -0.5, B, mask[h, :nqa], U16)
+            np.testing.assert_allclose(full[0][h][A], ref[0], rtol=1e-9, atol=1e-12)
+            _check(grads[0][h][torch.from_numpy(A.astype(np.int64)).cuda()], ref[0], most[0], mean[0], f"dq head {h}")
+            others = np.setdiff1d(np.arange(N), A)
+            assert not grads[0][h][torch.from_numpy(others).cuda()].any()
+        else:
+            ref, most, mean = _bounds(q6[h], k6[h], v6[h], o6[h], d6[h], l6[h], D ** -0.5, B, mask[h],
+                                      U16 if io == torch.float32 else 0.0)
+            _check(grads[0][h], ref[0], most[0], mean[0], f"dq head {h}")
+        np.testing.assert_allclose(full[1][h], ref[1], rtol=1e-9, atol=1e-12)
+        _check(grads[1][h], ref[1], most[1], mean[1], f"dk head {h}")
+        _check(grads[2][h], ref[2], most[2], mean[2], f"dv head {h}")
+
+
+@pytest.mark.gpu
+def test_same_bits_every_time_on_another_stream_and_replayed():
+    H, N, D, B = 3, 777, 128, 64
+    q, k, v, do = _inputs(H, N, D, 2)
+    nb = ops.nblocks(N, B)
+    bl = ops.BlockList.from_mask(torch.from_numpy(_mask(np.random.default_rng(1), H, nb, nb, 0.5)).cuda(), B)
+    bt = bl.transpose()
+    o, lse = ops.sparse_attn_fwd(q, k, v, bl, return_lse=True)
+    first = ops.sparse_attn_bwd(q, k, v, o, do, lse, bl, bt)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        again = ops.sparse_attn_bwd(q, k, v, o, do, lse, bl)
+    torch.cuda.synchronize()
+    graph, other = torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        replayed = ops.sparse_attn_bwd(q, k, v, o, do, lse, bl, bt)
+    with torch.cuda.graph(other):
+        replayed2 = ops.sparse_attn_bwd(q, k, v, o, do, lse, bl, bt)
+    graph.replay()
+    other.replay()
+    torch.cuda.synchronize()
+    for got in (again, replayed, replayed2):
+        assert all(torch.equal(x, y) for x, y in zip(first, got))
+    # new inputs in the captured buffers
+    do.copy_(do.flip(1))
+    graph.replay()
+    fresh = ops.sparse_attn_bwd(q, k, v, o, do, lse, bl, bt)
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(fresh, replayed))
+    assert not torch.equal(first[2], fresh[2])
+    ops.device_check()
+
+
+@pytest.mark.gpu
+def test_autograd_through_the_public_function():
+    H, F, Hl, Wl, D, B = 2, 2, 10, 15, 64, 64
+    N = F * Hl * Wl
+    q, k, v, do = _inputs(H, N, D, 4)
+    nb = ops.nblocks(N, B)
+    bl = ops.BlockList.from_mask(torch.from_numpy(_mask(np.random.default_rng(7), H, nb, nb, 0.5, holes=False)).cuda(), B)
+    leaves = [x.clone().requires_grad_() for x in (q, k, v)]
+    o = ops.sparse_attention(*leaves, bl)
+    assert torch.equal(o, ops.sparse_attn_fwd(q, k, v, bl, return_lse=True)[0])
+    o.backward(do.transpose(1, 2).contiguous().transpose(1, 2))                # a strided gradient
+    lse = ops.sparse_attn_fwd(q, k, v, bl, return_lse=True)[1]
+    for x, y in zip(leaves, ops.sparse_attn_bwd(q, k, v, o.detach(), do, lse, bl)):
+        assert torch.equal(x.grad, y)
+    # the slice mode, only some leaves, and an fp32 output
+    rep = ([True, False], F, Hl, Wl, 0, 3)
+    kk = k.clone().requires_grad_()
+    o = ops.sparse_attention(q, kk, v, bl, bl.transpose(), out_dtype=torch.float32, repeat=rep)
+    (g,) = torch.autograd.grad(o, kk, do.float())
+    o2, lse = ops.sparse_attn_fwd_repeat(q, k, v, bl, *rep, return_lse=True, out_dtype=torch.float32)
+    assert torch.equal(g, ops.sparse_attn_bwd_repeat(q, k, v, o2, do.float(), lse, bl, *rep)[1])
+    with pytest.raises(RuntimeError):
+        x = q.clone().requires_grad_()
+        (gq,) = torch.autograd.grad(ops.sparse_attention(x, k, v, bl).sum(), x, create_graph=True)
+        gq.sum().backward()                                                    # differentiable once
+
+
+@pytest.mark.gpu
+def test_refusals_on_the_gpu():
+    H, N, D, B = 1, 128, 64, 64
+    q, k, v, do = _inputs(H, N, D, 4)
+    bl = ops.BlockList.from_mask(torch.ones(H, 2, 2, dtype=torch.uint8, device="cuda"), B)
+    o, lse = ops.sparse_attn_fwd(q, k, v, bl, return_lse=True)
+    with pytest.raises(TypeError, match="dout"):
+        ops.sparse_attn_bwd(q, k, v, o, do.float(), lse, bl)
+    with pytest.raises(ValueError, match="contiguous"):
+        ops.sparse_attn_bwd(q, k, v, o, do.transpose(1, 2).contiguous().transpose(1, 2), lse, bl)
+    with pytest.raises(ValueError, match="shape"):
+        ops.sparse_attn_bwd(q, k, v, o, do, lse[:, :-1].contiguous(), bl)
+    with pytest.raises(TypeError, match="bf16 or fp32"):
+        ops.sparse_attn_bwd(q, k, v, o, do, lse, bl, grad_dtype=torch.float16)
+    with pytest.raises(ops.CalibError):
+        ops.sparse_attn_bwd(q, k, v, o, do, lse, ops.BlockList(H, 1, 1, 128, bl.row_ptr[:2].contiguous(), bl.col_idx), bl)
+    with pytest.raises(ops.CalibError):
+        ops.sparse_attn_bwd(q, k, v, o, do, lse, ops.BlockList(H, 2, 2, B, bl.row_ptr, bl.col_idx, bl.work[:1].contiguous()), bl)
+    with pytest.raises(ValueError, match="head_repeat"):
+        ops.sparse_attn_bwd_repeat(q, k, v, o, do, lse, bl, [True, False], 1, 2, 64, 0, 1)

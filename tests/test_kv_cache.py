@@ -1,0 +1,449 @@
+"""The 8-bit key/value cache: writing tokens into it and attention over it.
+
+CPU: the oracle's cached attention against its block-sparse attention, and the refusals that need no
+device.  GPU (marked): the kernels against the oracle.
+
+Tolerances of the attention, from fp16 weights (each off by at most 2^-11 of its value: u), logits whose
+fp32 sums are off by at most (D + 8) 2^-24 scale |q||k| (e; the exponential adds 2^-20), and sums of L terms:
+  |err O| <= (u + 2 e + L 2^-24) sum_c P_c |v_c| + u_out |O|,   |err LSE| <= e + L 2^-24 + 2^-22 (1 + |LSE|)
+with u_out = 2^-8 for bf16 results and 2^-24 for fp32 ones.  The queries and the cached values enter exactly.
+Scales of written blocks: one fp32 division (2^-24).  A written value is the nearest e4m3 of x / scale, computed
+as x * (1 / scale): off by at most half a step, 2^-4 of the value or 2^-10 below the normal range, and 3 2^-24
+more for the two roundings of the factor; a value rounded again when its block's scale grows gets that twice.
+"""
+import ctypes
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from calibrated_block_sparse_calib_b200 import ops
+from conftest import to64
+
+U32 = 2.0 ** -24
+
+
+def f8(t):
+    return t.to(torch.float32).cpu().numpy().astype(np.float64)
+
+
+# ------------------------------------------------------------------------------------
+# the oracle and the refusals (CPU)
+# ------------------------------------------------------------------------------------
+
+def test_oracle_cached_attention_is_sparse_attention_of_the_gathered_cache():
+    rng = np.random.default_rng(0)
+    S, Hkv, G, D, B, nb = 2, 2, 2, 8, 64, 4
+    pages = S * nb
+    k, v = (rng.standard_normal((pages, Hkv, B, D)) for _ in range(2))
+    ks, vs = (rng.random((pages, Hkv)) + 0.5 for _ in range(2))
+    table = rng.permutation(pages).reshape(S, nb)
+    lengths = np.array([3 * B + 11, B])
+    M = 20
+    q = rng.standard_normal((S, Hkv * G, M, D))
+    mask = (rng.random((Hkv, S, nb)) < 0.7).astype(np.uint8)
+    mask[:, :, 0] = 1
+    O, L, _ = oracle.cached_attention(q, k, v, ks, vs, table, lengths, [M, M], 0.3, False, mask)
+    for s in range(S):
+        n = lengths[s]
+        K, V = ((x[table[s]] * y[table[s]][:, :, None, None]).transpose(1, 0, 2, 3).reshape(Hkv, nb * B, D)[:, :n]
+                for x, y in ((k, ks), (v, vs)))
+        ref, lse = oracle.sparse_attention(q[s], K.repeat(G, 0), V.repeat(G, 0), 0.3, B,
+                                           mask[:, s:s + 1, : -(-n // B)].repeat(G, 0))
+        np.testing.assert_allclose(O[s], ref, rtol=1e-12)
+        np.testing.assert_allclose(L[s], lse, rtol=1e-12)
+    # the last new token sees every key; the one before sees all but the last
+    Oc, _, _ = oracle.cached_attention(q, k, v, ks, vs, table, lengths, [M, M], 0.3, True)
+    Of, _, _ = oracle.cached_attention(q, k, v, ks, vs, table, lengths, [M, M], 0.3, False)
+    Op, _, _ = oracle.cached_attention(q[:, :, M - 2:M - 1], k, v, ks, vs, table, lengths - 1, [1, 1], 0.3, True)
+    np.testing.assert_allclose(Oc[:, :, -1], Of[:, :, -1], rtol=1e-12)
+    np.testing.assert_allclose(Oc[:, :, M - 2], Op[:, :, 0], rtol=1e-12)
+
+
+def test_refusals_before_device_work():
+    L, null, fake = ops.lib(), ctypes.c_void_p(0), ctypes.c_void_p(256)
+    bad, unsupported = ops.CALIB_ERR_INVALID, ops.CALIB_ERR_UNSUPPORTED
+
+    def att(q=fake, k=fake, ks=fake, table=fake, o=fake, S=1, Hq=2, Hkv=2, M=1, D=64, B=64, nb=4, pages=4, scale=0.1,
+            flags=0, lse=null):
+        return L.sparse_attn_cached(q, k, fake, ks, fake, table, fake, null, o, lse, S, Hq, Hkv, M, D, B, nb, pages,
+                                    scale, None, flags, null, 0, null)
+
+    assert att(q=null) == att(k=null) == att(ks=null) == att(table=null) == att(o=null) == bad
+    assert att(q=ctypes.c_void_p(264)) == att(k=ctypes.c_void_p(264)) == att(table=ctypes.c_void_p(258)) == bad
+    assert att(lse=ctypes.c_void_p(258)) == att(flags=2) == att(scale=-1.0) == att(B=32) == bad
+    assert att(Hq=3) == att(Hq=1) == att(Hkv=0) == att(S=0) == att(M=0) == att(nb=0) == att(pages=0) == bad
+    assert att(D=80) == unsupported
+    assert att(pages=1 << 27) == att(nb=1 << 26) == unsupported
+
+    def write(k=fake, cache=fake, lengths=fake, S=1, Hkv=2, M=1, D=64, B=64, nb=4, pages=4):
+        return L.calib_cache_write(k, fake, cache, fake, fake, fake, fake, lengths, null, S, Hkv, M, D, B, nb, pages, null)
+
+    assert write(k=null) == write(cache=null) == write(lengths=null) == write(k=ctypes.c_void_p(264)) == bad
+    assert write(S=0) == write(M=0) == write(B=96) == write(pages=0) == bad
+    assert write(D=32) == write(pages=1 << 30) == unsupported
+    assert L.sparse_attn_cached_workspace(1, 3, 2, 1, 64, 64, 1) == L.sparse_attn_cached_workspace(0, 2, 2, 1, 64, 64, 1) == -1
+    assert L.sparse_attn_cached_workspace(1, 2, 2, 1, 64, 64, 1) == 0
+    assert L.sparse_attn_cached_workspace(1, 2, 2, 1, 64, 64, 1 << 16) > 0
+
+
+def test_host_tensors_and_malformed_caches_are_refused():
+    c = ops.KVCache.allocate(2, 1, 64, 64, device="cpu")
+    x = torch.zeros(1, 1, 1, 64, dtype=torch.bfloat16)
+    t, n = torch.zeros(1, 2, dtype=torch.int32), torch.ones(1, dtype=torch.int32)
+    with pytest.raises(TypeError, match="CUDA tensor"):
+        ops.sparse_attn_cached(x, c, t, n)
+    with pytest.raises(TypeError, match="CUDA tensor"):
+        ops.cache_write(c, x, x, t, n)
+
+
+# ------------------------------------------------------------------------------------
+# GPU
+# ------------------------------------------------------------------------------------
+
+def _cache(rng, S, Hkv, D, B, nb, spare=3):
+    """A cache with its pages handed out in random order, `spare` pages used by nobody."""
+    pages = S * nb + spare
+    g = torch.Generator().manual_seed(int(rng.integers(1 << 30)))
+    data = lambda: (torch.randn(pages, Hkv, B, D, generator=g) * 100).clamp_(-448, 448).to(torch.float8_e4m3fn).cuda()
+    scale = lambda: (0.005 + 0.01 * torch.rand(pages, Hkv, generator=g)).cuda()
+    table = torch.from_numpy(rng.permutation(pages)[:S * nb].reshape(S, nb).astype(np.int32)).cuda()
+    return ops.KVCache(data(), data(), scale(), scale()), table
+
+
+def _ints(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+def _check(got, lse, q, cache, table, lengths, new, scale, causal, mask=None):
+    q6, table = to64(q), table.cpu().numpy()
+    k, v, ks, vs = f8(cache.k), f8(cache.v), to64(cache.k_scale), to64(cache.v_scale)
+    k, v = np.nan_to_num(k), np.nan_to_num(v)                      # bytes behind the end are never weighed
+    O, L, A = oracle.cached_attention(q6, k, v, ks, vs, table, lengths, new, scale, causal, mask)
+    D, longest = q.shape[3], max(1, max(lengths))
+    qn = np.abs(q6).sum(-1).max(initial=0.0)
+    e = (D + 8) * U32 * scale * qn * float((np.abs(k).max((1, 2, 3)) * ks.max(1)).max()) + 2.0 ** -20
+    u_out = 2.0 ** -8 if got.dtype == torch.bfloat16 else U32
+    err = np.abs(to64(got) - O)
+    assert np.all(err <= (2.0 ** -11 + 2 * e + longest * U32) * A * (1 + u_out) + u_out * np.abs(O) + 2.0 ** -126), \
+        float((err / np.maximum(A, 1e-30)).max())
+    gl = to64(lse)
+    np.testing.assert_array_equal(np.isneginf(gl), np.isneginf(L))
+    fin = np.isfinite(L)
+    assert np.all(np.abs(gl[fin] - L[fin]) <= e + longest * U32 + 2.0 ** -22 * (1 + np.abs(L[fin])))
+    assert not to64(got)[~fin].any()
+
+
+CASES = [
+    # S, Hq, Hkv, M, D, B, lengths, new, causal, density
+    (1, 1, 1, 1, 64, 64, [1], None, True, None),
+    (1, 1, 1, 1, 128, 128, [1], None, True, None),
+    (2, 4, 4, 1, 128, 64, [64, 65], None, True, None),
+    (3, 8, 2, 1, 64, 128, [0, 127, 129], [0, 1, 1], True, None),
+    (4, 8, 1, 1, 128, 128, [31, 32, 33, 300], None, True, None),
+    (2, 10, 2, 1, 128, 128, [1500, 7], None, True, None),          # 5 heads per K/V head
+    (2, 12, 1, 1, 64, 64, [700, 260], None, True, None),           # 12 rows: the 16-row variant
+    (3, 6, 2, 5, 128, 64, [5, 200, 1027], [5, 3, 1], True, None),  # ragged new tokens, 15 rows
+    (2, 4, 2, 9, 64, 128, [9, 640], None, False, None),            # 18 rows: two row tiles, no causal limit
+    (2, 4, 2, 40, 128, 64, [40, 777], [40, 17], True, None),       # a short prompt: five row tiles
+    (3, 4, 4, 2, 128, 64, [700, 64, 1300], [2, 2, 1], True, 0.4),
+    (2, 8, 2, 1, 64, 64, [2000, 1111], None, True, 0.2),
+    (1, 2, 2, 1, 128, 128, [40000], None, True, None),             # split over many CTAs
+    (1, 16, 1, 3, 64, 64, [9001], None, True, 0.5),
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("S,Hq,Hkv,M,D,B,lengths,new,causal,density", CASES)
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_attention(S, Hq, Hkv, M, D, B, lengths, new, causal, density, dtype):
+    rng = np.random.default_rng(sum(lengths) + D + M)
+    nb = max(1, max(ops.nblocks(n, B) for n in lengths))
+    cache, table = _cache(rng, S, Hkv, D, B, nb)
+    q = torch.randn(S, Hq, M, D, generator=torch.Generator().manual_seed(1)).to(torch.bfloat16).cuda()
+    mask, bl = None, None
+    if density is not None:
+        mask = (rng.random((Hkv, S, nb)) < density).astype(np.uint8)
+        mask[0, 0] = 0                                             # a head that keeps nothing of a sequence
+        mask[-1, -1, -1] = 1                                       # the block that ends inside
+        bl = ops.BlockList.from_mask(torch.from_numpy(mask).cuda(), B)
+    o, lse = ops.sparse_attn_cached(q, cache, table, _ints(lengths), blist=bl, causal=causal, out_dtype=dtype,
+                                    new_lens=None if new is None else _ints(new), return_lse=True)
+    ops.device_check()
+    _check(o, lse, q, cache, table, lengths, [M] * S if new is None else new, D ** -0.5, causal, mask)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("D", [64, 128])
+def test_anything_behind_the_end_and_in_unused_pages(D):
+    """NaN and the largest values in the bytes behind each sequence's end, in unused pages and in their
+    scales; table entries past the end name no page."""
+    S, Hkv, B, nb = 2, 2, 64, 6
+    lengths = [65, 200]
+    rng = np.random.default_rng(D)
+    cache, table = _cache(rng, S, Hkv, D, B, nb)
+    q = torch.randn(S, 4, 2, D, generator=torch.Generator().manual_seed(2)).to(torch.bfloat16).cuda()
+    clean = ops.sparse_attn_cached(q, cache, table, _ints(lengths), return_lse=True)
+    used = {int(table[s, b]): min(B, lengths[s] - b * B) for s in range(S) for b in range(ops.nblocks(lengths[s], B))}
+    kb, vb = cache.k.view(torch.uint8), cache.v.view(torch.uint8)
+    for page in range(cache.k.shape[0]):
+        n = used.get(page, 0)
+        kb[page, :, n:] = 0x7F                                     # NaN
+        vb[page, :, n:] = 0xFF
+        if n == 0:
+            cache.k_scale[page] = math.nan
+            cache.v_scale[page] = math.inf
+    for s in range(S):
+        table[s, ops.nblocks(lengths[s], B):] = 2 ** 31 - 1
+    dirty = ops.sparse_attn_cached(q, cache, table, _ints(lengths), return_lse=True)
+    ops.device_check()
+    assert torch.equal(clean[0], dirty[0]) and torch.equal(clean[1], dirty[1])
+
+
+@pytest.mark.gpu
+def test_values_of_every_size():
+    """Logits of +-200 from queries of 2^-60 and 2^60 against scales that undo it, weights down to 2^-35 of
+    the largest, a scale of 0, and queries of 0."""
+    S, H, D, B = 1, 4, 64, 64
+    rng = np.random.default_rng(3)
+    cache, table = _cache(rng, S, H, D, B, 8)
+    q = torch.randn(S, H, 2, D, generator=torch.Generator().manual_seed(3)) * 4
+    q[:, 0] *= 2.0 ** -60
+    q[:, 1] *= 2.0 ** 60
+    q[:, 2, 0] = 0
+    cache.k_scale[:, 0] *= 2.0 ** 60
+    cache.k_scale[:, 1] *= 2.0 ** -60
+    cache.v_scale[int(table[0, 3]), 2] = 0.0
+    q = q.to(torch.bfloat16).cuda()
+    o, lse = ops.sparse_attn_cached(q, cache, table, _ints([500]), return_lse=True, out_dtype=torch.float32)
+    k, v, ks, vs = f8(cache.k), f8(cache.v), to64(cache.k_scale), to64(cache.v_scale)
+    O, L, A = oracle.cached_attention(to64(q), k, v, ks, vs, table.cpu().numpy(), [500], [2], D ** -0.5, True)
+    # e as above, head by head: |q||k| of each head's own sizes
+    for h in range(H):
+        e = (D + 8) * U32 * D ** -0.5 * float(np.abs(to64(q))[0, h].sum(-1).max()) * 448 * ks[:, h].max() + 2.0 ** -20
+        assert np.all(np.abs(to64(o)[0, h] - O[0, h]) <= (2.0 ** -11 + 2 * e + 500 * U32) * A[0, h] + U32 * np.abs(O[0, h]))
+        assert np.all(np.abs(to64(lse)[0, h] - L[0, h]) <= e + 500 * U32 + 2.0 ** -22 * (1 + np.abs(L[0, h])))
+
+
+@pytest.mark.gpu
+def test_bad_lengths_and_pages_are_reported_and_left_out():
+    """Out-of-range values are turned into a status by the kernels' own checks: the sequence or block is left
+    out, the others are as before."""
+    S, H, D, B, nb = 3, 2, 64, 64, 4
+    rng = np.random.default_rng(4)
+    cache, table = _cache(rng, S, H, D, B, nb)
+    q = torch.randn(S, H, 1, D, generator=torch.Generator().manual_seed(4)).to(torch.bfloat16).cuda()
+    good = ops.sparse_attn_cached(q, cache, table, _ints([100, 200, 256]))
+    for lengths, new in (([100, 257, 256], [1, 1, 1]), ([100, -1, 256], [1, 0, 1]), ([100, 200, 256], [1, 2, 1])):
+        o = ops.sparse_attn_cached(q, cache, table, _ints(lengths), new_lens=_ints(new))
+        with pytest.raises(ops.CalibError):
+            ops.device_check()
+        assert not o[1].any() and torch.equal(o[0], good[0]) and torch.equal(o[2], good[2])
+    broken = table.clone()
+    broken[1, 3], broken[2, 1] = cache.k.shape[0], -1
+    o = ops.sparse_attn_cached(q, cache, broken, _ints([100, 200, 256]))
+    with pytest.raises(ops.CalibError):
+        ops.device_check()
+    assert torch.equal(o[0], good[0])
+    before = [x.clone() for x in (cache.k.view(torch.uint8), cache.k_scale)]
+    x = torch.ones(S, H, 1, D, dtype=torch.bfloat16, device="cuda")
+    ops.cache_write(cache, x, x, table, _ints([257, -3, 10]), new_lens=_ints([1, 1, 11]))
+    with pytest.raises(ops.CalibError):
+        ops.device_check()
+    broken[:] = 1 << 30
+    ops.cache_write(cache, x, x, broken, _ints([5, 6, 7]))
+    with pytest.raises(ops.CalibError):
+        ops.device_check()
+    assert torch.equal(before[0], cache.k.view(torch.uint8)) and torch.equal(before[1], cache.k_scale)
+
+
+def _expected_write(cache, table, kx, vx, lengths, new, B):
+    """What the cache stands for after the write (64 bits), each value's allowance, and which bytes may change."""
+    out = []
+    for data, scales, x in ((cache.k, cache.k_scale, kx), (cache.v, cache.v_scale, vx)):
+        val, sc, tol = f8(data), to64(scales).copy(), None
+        tol = np.zeros(val.shape)
+        touched = np.zeros(val.shape, bool)
+        xs = to64(x)
+        for s, (n, m) in enumerate(zip(lengths, new)):
+            for b in range((n - m) // B if m else 0, -(-n // B) if m else 0):
+                page = int(table[s, b])
+                lo, hi = max(n - m - b * B, 0), min(n - b * B, B)
+                for h in range(val.shape[1]):
+                    tok = xs[s, h, b * B + lo - (n - m): b * B + hi - (n - m)]
+                    held = sc[page, h]
+                    scale = oracle.cache_scales(tok, held, lo, hi)
+                    step = lambda y: np.maximum(2.0 ** -4 * np.abs(y), 2.0 ** -10) + 4 * U32 * np.abs(y)
+                    clipped = np.clip(np.nan_to_num(tok, nan=0.0, posinf=1e300, neginf=-1e300), -448 * scale, 448 * scale)
+                    val[page, h, lo:hi] = clipped / scale
+                    tol[page, h, lo:hi] = step(clipped / scale)
+                    touched[page, h, lo:hi] = True
+                    if lo > 0 and scale > held:
+                        val[page, h, :lo] *= held / scale
+                        tol[page, h, :lo] = step(val[page, h, :lo])
+                        touched[page, h, :lo] = True
+                    sc[page, h] = scale
+        out.append((val, sc, tol, touched))
+    return out
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("S,Hkv,M,D,B,lengths,new", [
+    (1, 1, 1, 64, 64, [1], None), (2, 3, 1, 128, 128, [64, 129], None), (3, 2, 7, 64, 64, [64, 70, 0], [7, 3, 0]),
+    (2, 2, 200, 128, 64, [200, 333], [200, 131]), (2, 1, 300, 64, 128, [511, 300], [300, 1]),
+    (1, 2, 128, 128, 128, [256], None), (4, 8, 2, 128, 128, [3, 128, 129, 130], [2, 2, 2, 1])])
+def test_write(S, Hkv, M, D, B, lengths, new):
+    rng = np.random.default_rng(sum(lengths))
+    nb = max(ops.nblocks(n, B) for n in lengths) + 1
+    cache, table = _cache(rng, S, Hkv, D, B, nb)
+    g = torch.Generator().manual_seed(5)
+    kx, vx = ((torch.randn(S, Hkv, M, D, generator=g) * 2.0 ** torch.randint(-3, 3, (S, Hkv, 1, 1), generator=g))
+              .to(torch.bfloat16).cuda() for _ in range(2))
+    use = [M] * S if new is None else new
+    for s in range(S):                                             # padding slots are not read
+        kx[s, :, use[s]:] = math.nan
+    want = _expected_write(cache, table.cpu().numpy(), kx, vx, lengths, use, B)
+    before = cache.k.view(torch.uint8).clone(), cache.v.view(torch.uint8).clone()
+    ops.cache_write(cache, kx, vx, table, _ints(lengths), new_lens=None if new is None else _ints(new))
+    ops.device_check()
+    for data, scales, old, (val, sc, tol, touched) in zip((cache.k, cache.v), (cache.k_scale, cache.v_scale), before, want):
+        assert np.all(np.abs(to64(scales) - sc) <= U32 * sc)
+        got = f8(data)
+        assert np.all(np.abs(got - val)[touched] <= tol[touched])
+        assert np.array_equal(data.view(torch.uint8).cpu().numpy()[~touched], old.cpu().numpy()[~touched])
+    # writing the same again changes nothing
+    after = [x.clone() for x in (cache.k.view(torch.uint8), cache.v.view(torch.uint8), cache.k_scale, cache.v_scale)]
+    ops.cache_write(cache, kx, vx, table, _ints(lengths), new_lens=None if new is None else _ints(new))
+    now = cache.k.view(torch.uint8), cache.v.view(torch.uint8), cache.k_scale, cache.v_scale
+    assert all(torch.equal(x, y) for x, y in zip(after, now))
+
+
+@pytest.mark.gpu
+def test_write_of_zeros_infinities_and_tiny_values():
+    S, Hkv, M, D, B = 1, 4, 4, 64, 64
+    cache, table = _cache(np.random.default_rng(6), S, Hkv, D, B, 1)
+    x = torch.zeros(S, Hkv, M, D, dtype=torch.bfloat16)
+    x[0, 1] = 2.0 ** -130                                          # far below the smallest scale
+    x[0, 2, :, 0], x[0, 2, 0, 1], x[0, 2, 1, 2] = 3.0, math.inf, -math.inf
+    x[0, 3, 0, 0], x[0, 3, 0, 1] = math.nan, 448.0
+    x = x.cuda()
+    ops.cache_write(cache, x, x, table, _ints([M]))
+    ops.device_check()
+    page = int(table[0, 0])
+    got, sc = f8(cache.k)[page], to64(cache.k_scale)[page]
+    tiny = np.float64(np.float32(2.0 ** -100) / np.float32(448.0))
+    assert not got[0, :M].any() and sc[0] == tiny
+    assert not got[1, :M].any() and sc[1] == tiny
+    assert got[2, 0, 1] == 448 and got[2, 1, 2] == -448 and abs(got[2, 0, 0]) == 448 and abs(sc[2] - 3 / 448) < 1e-8
+    assert math.isnan(got[3, 0, 0]) and got[3, 0, 1] == 448 and sc[3] == 1.0
+
+
+@pytest.mark.gpu
+def test_tokens_written_one_by_one_then_attended_to():
+    """A sequence grown token by token (blocks filling up, scales growing), attended to after each token, next to a
+    sequence written as one prompt."""
+    Hkv, G, D, B, nb = 2, 2, 64, 64, 3
+    steps = 70
+    g = torch.Generator().manual_seed(7)
+    kx, vx = ((torch.randn(2, Hkv, steps, D, generator=g) * (1 + torch.arange(steps)[:, None] / 20)).to(torch.bfloat16).cuda()
+              for _ in range(2))
+    q = torch.randn(2, Hkv * G, steps, D, generator=g).to(torch.bfloat16).cuda()
+    cache = ops.KVCache.allocate(2 * nb, Hkv, B, D)
+    table = _ints([[0, 2, 4], [5, 3, 1]])
+    slots = [x[1:].clone().repeat(2, 1, 1, 1).contiguous() for x in (kx, vx)]
+    ops.cache_write(cache, *slots, table, _ints([0, steps]), new_lens=_ints([0, steps]))     # slot 0 is free
+    prompt = ops.sparse_attn_cached(q, cache, table, _ints([0, steps]), new_lens=_ints([0, steps]))
+    assert not prompt[0].any()
+    for n in range(1, steps + 1):
+        new = [x[:, :, n - 1:n].contiguous() for x in (kx, vx)]
+        ops.cache_write(cache, *new, table, _ints([n, steps]), new_lens=_ints([1, 0]))
+        o, lse = ops.sparse_attn_cached(q[:, :, n - 1:n].contiguous(), cache, table, _ints([n, steps]),
+                                        new_lens=_ints([1, 1]), return_lse=True)
+        if n in (1, 2, 33, 64, 65, steps):
+            _check(o, lse, q[:, :, n - 1:n], cache, table, [n, steps], [1, 1], D ** -0.5, True)
+    ops.device_check()
+    # the values that the cache stands for are those that were written: the block's largest magnitude over 448 is
+    # its scale, and every rounding (one per growth of the scale, at most) is within half a step of it
+    for data, scales, x in ((cache.k, cache.k_scale, kx), (cache.v, cache.v_scale, vx)):
+        for b, page in enumerate((0, 2)):
+            n = min(B, steps - b * B)
+            want = to64(x[0, :, b * B:b * B + n])
+            assert np.all(np.abs(to64(scales)[page] - np.abs(want).max((1, 2)) / 448) <= 2 * U32 * to64(scales)[page])
+    assert torch.equal(prompt[1], ops.sparse_attn_cached(q, cache, table, _ints([0, steps]), new_lens=_ints([0, steps]))[1])
+
+
+@pytest.mark.gpu
+def test_same_bits_on_another_stream_and_replayed():
+    S, Hq, Hkv, D, B = 2, 4, 2, 128, 64
+    cache, table = _cache(np.random.default_rng(8), S, Hkv, D, B, 60)
+    lengths = _ints([3800, 100])
+    q = torch.randn(S, Hq, 1, D, generator=torch.Generator().manual_seed(8)).to(torch.bfloat16).cuda()
+    call = lambda: ops.sparse_attn_cached(q, cache, table, lengths, return_lse=True)
+    first = call()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        again = call()
+    torch.cuda.synchronize()
+    graphs, outs = [torch.cuda.CUDAGraph() for _ in range(2)], []
+    for graph in graphs:
+        with torch.cuda.graph(graph):
+            outs.append(call())
+    for graph in graphs:
+        graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for got in (again, *outs) for a, b in zip(first, got))
+    lengths.copy_(_ints([1234, 3840]))
+    graphs[0].replay()
+    fresh = call()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(fresh, outs[0]))
+
+
+@pytest.mark.gpu
+def test_a_cache_past_32_bit_offsets():
+    """5 GB of keys: the pages at the far end are read and written at their own place."""
+    Hkv, D, B = 8, 128, 128
+    pages = (5 << 30) // (Hkv * B * D)
+    k = torch.zeros(pages, Hkv, B, D, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)
+    v = torch.zeros(pages, Hkv, B, D, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)
+    cache = ops.KVCache(k, v, *(torch.zeros(pages, Hkv, device="cuda") for _ in range(2)))
+    table = _ints([[pages - 1, 0, pages - 2]])
+    g = torch.Generator().manual_seed(9)
+    kx, vx = (torch.randn(1, Hkv, 300, D, generator=g).to(torch.bfloat16).cuda() for _ in range(2))
+    ops.cache_write(cache, kx, vx, table, _ints([300]))
+    q = torch.randn(1, Hkv, 1, D, generator=g).to(torch.bfloat16).cuda()
+    o, lse = ops.sparse_attn_cached(q, cache, table, _ints([300]), return_lse=True)
+    ops.device_check()
+    small = ops.KVCache(*(x[[0, pages - 2, pages - 1]].contiguous() if x.dtype == torch.float32 else
+                          x.view(torch.uint8)[[0, pages - 2, pages - 1]].contiguous().view(torch.float8_e4m3fn)
+                          for x in (cache.k, cache.v, cache.k_scale, cache.v_scale)))
+    _check(o, lse, q, small, _ints([[2, 0, 1]]), [300], [1], D ** -0.5, True)
+    assert not cache.k.view(torch.uint8)[1:pages - 2].any()
+
+
+@pytest.mark.gpu
+def test_refusals_on_the_gpu():
+    S, H, D, B = 1, 2, 64, 64
+    cache, table = _cache(np.random.default_rng(1), S, H, D, B, 2)
+    q = torch.zeros(S, H, 1, D, dtype=torch.bfloat16, device="cuda")
+    n = _ints([70])
+    with pytest.raises(TypeError, match="q must be"):
+        ops.sparse_attn_cached(q.half(), cache, table, n)
+    with pytest.raises(ValueError, match="shape"):
+        ops.sparse_attn_cached(q, cache, table, _ints([1, 2]))
+    with pytest.raises(ValueError, match="block_table"):
+        ops.sparse_attn_cached(q, cache, table[0], n)
+    with pytest.raises(TypeError, match="lengths"):
+        ops.sparse_attn_cached(q, cache, table, n.long())
+    with pytest.raises(TypeError, match="bf16 or fp32"):
+        ops.sparse_attn_cached(q, cache, table, n, out_dtype=torch.float16)
+    with pytest.raises(ops.CalibError):                            # a list of another shape
+        ops.sparse_attn_cached(q, cache, table, n, blist=ops.BlockList.from_mask(
+            torch.ones(H, S, 3, dtype=torch.uint8, device="cuda"), B))
+    with pytest.raises(ops.CalibError):                            # query heads that do not share evenly
+        ops.sparse_attn_cached(torch.zeros(S, 3, 1, D, dtype=torch.bfloat16, device="cuda"), cache, table, n)
+    with pytest.raises(ValueError, match="shape"):
+        ops.cache_write(cache, q[:, :1].contiguous(), q, table, n)
