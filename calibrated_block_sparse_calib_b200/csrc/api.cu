@@ -307,13 +307,14 @@ calib_status launch_sim(const CUtensorMap& tk, const calib::SimParams& p, int gr
 // Workspace of sparse_attn_bwd(_repeat): row statistics over whole blocks, dO as bf16 (fp32 in and
 // out only), and the anchors' rows of Q and dO (repeat heads only).
 struct BwdSpace {
-    size_t stats, do16, qa, doa, total;
+    size_t ndelta, do16, qa, doa, total;   // nlse is at 0
 };
 BwdSpace bwd_space(int H, int N, int D, int B, long long n_anchor, bool io_f32) {
     auto up = [](size_t x) { return (x + 255) & ~static_cast<size_t>(255); };
     BwdSpace w{};
     const size_t rows = static_cast<size_t>(cdiv(N, B)) * B;
-    w.do16 = up(H * rows * sizeof(float2));
+    w.ndelta = up(H * rows * 4);
+    w.do16 = 2 * w.ndelta;
     w.qa = w.do16 + (io_f32 ? up(static_cast<size_t>(H) * N * D * 2) : 0);
     const size_t anchors = n_anchor ? up(static_cast<size_t>(H) * n_anchor * D * 2) : 0;
     w.doa = w.qa + anchors;
@@ -321,15 +322,26 @@ BwdSpace bwd_space(int H, int N, int D, int B, long long n_anchor, bool io_f32) 
     return w;
 }
 
+struct BwdMaps {
+    CUtensorMap k, v, q, dout, qa, doa;
+};
+
 template <int D, int BLK>
-calib_status launch_bwd(const calib::BwdParams& p, cudaStream_t st) {
+calib_status launch_bwd(const BwdMaps& m, const calib::BwdParams& p, cudaStream_t st) {
+    constexpr int ST = 2;   // ring depth (with the two resident tiles, 194 KB at D = B = 128)
+    using L = calib::BwdSmem<D, BLK, ST>;
+    static_assert(L::BYTES <= 232448, "shared memory budget");
     const int rows = p.geo.nq * BLK;
     const long long threads = static_cast<long long>(p.geo.H) * rows * (D / 8);
+    auto* fq = calib::bwd_q_kernel<D, BLK, ST>;
+    auto* fkv = calib::bwd_kv_kernel<D, BLK, ST>;
+    if (calib_status s = ensure_smem(reinterpret_cast<const void*>(fq), L::BYTES)) return s;
+    if (calib_status s = ensure_smem(reinterpret_cast<const void*>(fkv), L::BYTES)) return s;
     calib::bwd_prepare_kernel<D><<<static_cast<int>((threads + 255) / 256), 256, 0, st>>>(p, rows);
     if (calib_status s = launch_status()) return s;
-    calib::bwd_simple_kernel<D, BLK, false><<<dim3(p.geo.nq * (BLK / 8), p.geo.H), 256, 0, st>>>(p);
+    fkv<<<p.geo.H * p.geo.nk, calib::kBwdThreads, L::BYTES, st>>>(m.k, m.v, m.q, m.dout, m.qa, m.doa, p);
     if (calib_status s = launch_status()) return s;
-    calib::bwd_simple_kernel<D, BLK, true><<<dim3(p.geo.nk * (BLK / 8), p.geo.H), 256, 0, st>>>(p);
+    fq<<<p.geo.H * p.geo.nq, calib::kBwdThreads, L::BYTES, st>>>(m.k, m.v, m.q, m.dout, m.qa, m.doa, p);
     return launch_status();
 }
 
@@ -364,21 +376,32 @@ calib_status bwd_common(const void* q, const void* k, const void* v, const void*
     p.dout = dout;
     p.lse = lse;
     p.dq = dq; p.dk = dk; p.dv = dv;
-    p.stats = reinterpret_cast<float2*>(base + w.stats);
+    p.nlse = reinterpret_cast<float*>(base);
+    p.ndelta = reinterpret_cast<float*>(base + w.ndelta);
     p.io_f32 = c.p.out_f32;
     p.do16 = p.io_f32 ? reinterpret_cast<__nv_bfloat16*>(base + w.do16)
                       : static_cast<__nv_bfloat16*>(const_cast<void*>(dout));
     p.qa = reinterpret_cast<__nv_bfloat16*>(base + w.qa);
     p.doa = reinterpret_cast<__nv_bfloat16*>(base + w.doa);
-    p.row_ptr = list->row_ptr; p.col_idx = list->col_idx; p.work = list->work; p.n_work = list->n_work;
-    p.t_row_ptr = list_t->row_ptr; p.t_col_idx = list_t->col_idx; p.t_work = list_t->work; p.n_t_work = list_t->n_work;
+    p.row_ptr = list->row_ptr; p.col_idx = list->col_idx; p.work = list->work;
+    p.t_row_ptr = list_t->row_ptr; p.t_col_idx = list_t->col_idx; p.t_work = list_t->work;
     p.geo = c.p;
     p.scale = scale;
     p.grad_f32 = (flags & CALIB_ATTN_GRAD_F32) ? 1 : 0;
     p.timeout_ns = kDefaultTimeoutNs;
+    BwdMaps m;
+    m.k = c.tk;
+    m.v = c.tv;
+    m.q = c.tq;
+    if (!make_tmap(&m.dout, p.do16, D, N, H, c.B)) return CALIB_ERR_CUDA;
+    m.qa = m.q;
+    m.doa = m.dout;
+    if (repeat_bits && (!make_tmap(&m.qa, p.qa, D, c.p.n_anchor, H, c.B) ||
+                        !make_tmap(&m.doa, p.doa, D, c.p.n_anchor, H, c.B)))
+        return CALIB_ERR_CUDA;
     cudaStream_t st = as_stream(stream);
-    if (D == 128) return c.B == 128 ? launch_bwd<128, 128>(p, st) : launch_bwd<128, 64>(p, st);
-    return c.B == 128 ? launch_bwd<64, 128>(p, st) : launch_bwd<64, 64>(p, st);
+    if (D == 128) return c.B == 128 ? launch_bwd<128, 128>(m, p, st) : launch_bwd<128, 64>(m, p, st);
+    return c.B == 128 ? launch_bwd<64, 128>(m, p, st) : launch_bwd<64, 64>(m, p, st);
 }
 
 // ---- 8-bit cache -------------------------------------------------------------------

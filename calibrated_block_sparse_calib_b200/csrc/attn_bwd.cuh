@@ -11,13 +11,12 @@ struct BwdParams {
     const void *o, *dout;                // [H, N, D] bf16, or fp32 when io_f32
     const float* lse;                    // [H, N] natural log
     void *dq, *dk, *dv;                  // [H, N, D] bf16, or fp32 when grad_f32
-    float2* stats;                       // workspace [H, nq * BLK]: (LSE / ln 2, delta)
+    float *nlse, *ndelta;                // workspace [H, nq * BLK]: -LSE / ln 2 and -delta
     __nv_bfloat16* do16;                 // workspace [H, N, D] (io_f32), else dout itself
     __nv_bfloat16 *qa, *doa;             // workspace [H, n_anchor, D] (repeat heads) or nullptr
     const int32_t *row_ptr, *t_row_ptr;
     const int16_t *col_idx, *t_col_idx;
     const int32_t *work, *t_work;
-    int n_work, n_t_work;
     AttnParams geo;                      // H, N, nq, nk, scale_log2 and the repeat geometry
     float scale;
     int io_f32, grad_f32;
@@ -34,12 +33,12 @@ __device__ __forceinline__ int anchor_copies(const AttnParams& p, int a) {
     return min(p.stride, p.Hl - ((a / p.Wl) % p.Ar) * p.stride);
 }
 
-// Row statistics (LSE / ln 2, delta = sum_d dO O), one group of D/8 threads per query row, and the
-// operands that the products need as bf16: dO when it came as fp32, and for a repeat head the
+// Row statistics (-LSE / ln 2 and -delta, delta = sum_d dO O), one group of D/8 threads per query
+// row, and the operands that the products need as bf16: dO when it came as fp32, and for a repeat head the
 // anchors' rows of Q with dO and delta summed over the tokens that take the anchor's output (its O
 // and LSE are the same in all of them).  The sum is fp32 and dO enters the products as bf16, so it
-// is rounded once (2^-9 relative), as P and dS are.  Rows past the sequence get LSE = +inf, which
-// makes their probabilities 0; so do rows with nothing kept (LSE = -inf).
+// is rounded once (2^-9 relative), as P and dS are.  Rows past the sequence get -LSE = -inf, which
+// makes their probabilities 0; so do rows with nothing kept.
 // Reads dO and O once: 2 x 268 MB at 12 x 32760 x 128, bound by memory.
 template <int D>
 __global__ void __launch_bounds__(256) bwd_prepare_kernel(const BwdParams p, int rows_padded) {
@@ -51,7 +50,7 @@ __global__ void __launch_bounds__(256) bwd_prepare_kernel(const BwdParams p, int
     if (h >= g.H) return;                                 // whole rows: TPR divides 256
     const bool rep = repeats(g, h);
     const int Nq = rep ? g.n_anchor : g.N;
-    float acc = 0.f, lse = INFINITY;
+    float acc = 0.f, nlse = -INFINITY;
     if (r < Nq) {
         const int tok = rep ? anchor_token(g, r) : r;
         const int n = rep ? anchor_copies(g, r) : 1;
@@ -98,97 +97,661 @@ __global__ void __launch_bounds__(256) bwd_prepare_kernel(const BwdParams p, int
             }
         }
         const float l = p.lse[static_cast<size_t>(h) * g.N + tok];
-        lse = l == -INFINITY ? INFINITY : l * 1.4426950408889634f;
+        if (l != -INFINITY) nlse = -l * 1.4426950408889634f;
     }
 #pragma unroll
     for (int off = TPR / 2; off > 0; off >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, off);
-    if (part == 0) p.stats[static_cast<size_t>(h) * rows_padded + r] = make_float2(lse, acc);
+    if (part == 0) {
+        p.nlse[static_cast<size_t>(h) * rows_padded + r] = nlse;
+        p.ndelta[static_cast<size_t>(h) * rows_padded + r] = -acc;
+    }
 }
 
-// One warp per row of a block: KV = false, the row is a query and the columns are its kept keys
-// (dQ); KV = true, the row is a key and the columns are the queries that keep it (dK, dV).
-// s = a.c and dp = b.e for a lane's column, p = 2^(s - LSE), ds = p (dp - delta); then
-// out1 += ds c, out2 += p e with the lanes over D.
-template <int D, int BLK, bool KV>
-__global__ void __launch_bounds__(256) bwd_simple_kernel(const BwdParams p) {
-    constexpr int LD = D + 2, SUB = 32;
-    __shared__ __nv_bfloat16 sc[SUB * LD], se[SUB * LD];
-    __shared__ float sa[8][D], sb[8][D];
-    const AttnParams& g = p.geo;
-    const int nrow = KV ? g.nk : g.nq;
-    const int h = blockIdx.y, i = blockIdx.x / (BLK / 8), sub = blockIdx.x % (BLK / 8);
-    const int warp = static_cast<int>(warp_id()), lane = static_cast<int>(lane_id());
-    const bool rep = repeats(g, h);
-    const int Nq = rep ? g.n_anchor : g.N;
-    const __nv_bfloat16* q = rep ? p.qa + static_cast<size_t>(h) * g.n_anchor * D : p.q + static_cast<size_t>(h) * g.N * D;
-    const __nv_bfloat16* dO = rep ? p.doa + static_cast<size_t>(h) * g.n_anchor * D : p.do16 + static_cast<size_t>(h) * g.N * D;
-    const __nv_bfloat16* k = p.k + static_cast<size_t>(h) * g.N * D;
-    const __nv_bfloat16* v = p.v + static_cast<size_t>(h) * g.N * D;
-    const __nv_bfloat16 *A = KV ? k : q, *Bm = KV ? v : dO, *C = KV ? q : k, *E = KV ? dO : v;
-    const int rows = KV ? g.N : Nq, cols = KV ? Nq : g.N;
-    const int r = i * BLK + sub * 8 + warp;
-    for (int d = lane; d < D; d += 32) {
-        sa[warp][d] = r < rows ? __bfloat162float(A[static_cast<size_t>(r) * D + d]) : 0.f;
-        sb[warp][d] = r < rows ? __bfloat162float(Bm[static_cast<size_t>(r) * D + d]) : 0.f;
+constexpr int kBwdThreads = 320;          // warp 0 TMA, warp 1 MMA, warps 2..9 arithmetic
+constexpr int kBwdArith = 256;
+constexpr uint32_t kBwdTmemS = 0;         // S (fp32, BLK columns)
+constexpr uint32_t kBwdTmemDP = 128;      // dP (fp32, BLK columns)
+constexpr uint32_t kBwdTmemAcc = 256;     // the accumulators, D columns each
+
+// (d0, d1) = (a0, a1) * (b0, b1), packed fp32x2
+__device__ __forceinline__ void fmul2(float& d0, float& d1, float a0, float a1, float b0, float b1) {
+    asm("{\n\t.reg .b64 ra, rb, rd;\n\t"
+        "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
+        "mul.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+        : "=f"(d0), "=f"(d1)
+        : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
+}
+// Untiled bulk copy global -> shared memory: both addresses and the size multiples of 16 bytes.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar)
+                 : "memory");
+}
+// This thread's HC columns of a TMEM tile, as floats.
+template <int HC>
+__device__ __forceinline__ void tmem_row(uint32_t taddr, float (&x)[HC]) {
+    uint32_t raw[HC];
+    if constexpr (HC == 64) tmem_ld64_wait(taddr, raw);
+    else tmem_ld32_wait(taddr, raw);
+#pragma unroll
+    for (int c = 0; c < HC; ++c) x[c] = __uint_as_float(raw[c]);
+}
+// HC values packed as bf16 pairs into HC / 2 TMEM columns.
+template <int HC>
+__device__ __forceinline__ void tmem_put(uint32_t taddr, const uint32_t (&pk)[HC / 2]) {
+    if constexpr (HC == 64) tmem_st32(taddr, pk);
+    else tmem_st16(taddr, pk);
+}
+// 32 accumulator columns of one row, scaled, to a gradient row (bf16 or fp32).
+__device__ __forceinline__ void put_grad32(void* base, size_t at, bool f32, uint32_t taddr, float scale, bool any, bool write) {
+    uint32_t raw[32];
+    if (any) {
+        tmem_ld32_wait(taddr, raw);
+#pragma unroll
+        for (int e = 0; e < 32; ++e) raw[e] = __float_as_uint(__uint_as_float(raw[e]) * scale);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 32; ++e) raw[e] = 0u;
     }
-    const float2* stats = p.stats + static_cast<size_t>(h) * g.nq * BLK;
-    const float2 own = !KV && r < rows ? stats[r] : make_float2(INFINITY, 0.f);
-    float o1[D / 32], o2[D / 32];
+    if (!write) return;
+    if (f32) {
+        store_row32_f32(static_cast<float*>(base) + at, raw);
+    } else {
+        uint32_t packed[16];
 #pragma unroll
-    for (int x = 0; x < D / 32; ++x) o1[x] = o2[x] = 0.f;
-    const int32_t* rp = KV ? p.t_row_ptr : p.row_ptr;
-    const int16_t* ci = KV ? p.t_col_idx : p.col_idx;
-    const int beg = rp[h * nrow + i], end = i * BLK < rows ? rp[h * nrow + i + 1] : beg;
-    for (int x = beg; x < end; ++x) {
-        const int j = ci[x];
-        for (int c0 = 0; c0 < BLK; c0 += SUB) {
-            __syncthreads();
-            for (int y = threadIdx.x; y < SUB * D / 2; y += 256) {
-                const int c = y / (D / 2), d = y % (D / 2) * 2;
-                const int n = j * BLK + c0 + c;
-                uint32_t w0 = 0, w1 = 0;
-                if (j >= 0 && n < cols) {
-                    w0 = *reinterpret_cast<const uint32_t*>(C + static_cast<size_t>(n) * D + d);
-                    w1 = *reinterpret_cast<const uint32_t*>(E + static_cast<size_t>(n) * D + d);
-                }
-                *reinterpret_cast<uint32_t*>(sc + c * LD + d) = w0;
-                *reinterpret_cast<uint32_t*>(se + c * LD + d) = w1;
-            }
-            __syncthreads();
-            float s = 0.f, dp = 0.f;
-            for (int d = 0; d < D; ++d) {
-                s += sa[warp][d] * __bfloat162float(sc[lane * LD + d]);
-                dp += sb[warp][d] * __bfloat162float(se[lane * LD + d]);
-            }
-            const int n = j * BLK + c0 + lane;
-            const bool ok = j >= 0 && n < cols;
-            const float2 st = KV ? (ok ? stats[n] : make_float2(INFINITY, 0.f)) : own;
-            const float pr = ok ? exp2f(s * g.scale_log2 - st.x) : 0.f;
-            const float ds = pr * (dp - st.y);
-            for (int c = 0; c < SUB; ++c) {
-                const float pc = __shfl_sync(0xffffffffu, pr, c), dc = __shfl_sync(0xffffffffu, ds, c);
-#pragma unroll
-                for (int y = 0; y < D / 32; ++y) {
-                    o1[y] += dc * __bfloat162float(sc[c * LD + y * 32 + lane]);
-                    if (KV) o2[y] += pc * __bfloat162float(se[c * LD + y * 32 + lane]);
+        for (int e = 0; e < 16; ++e) packed[e] = pack_bf16x2(__uint_as_float(raw[2 * e]), __uint_as_float(raw[2 * e + 1]));
+        store_row32_bf16(static_cast<__nv_bfloat16*>(base) + at, packed);
+    }
+}
+
+// The work item of a CTA: head, block, and its list row.  False: nothing to write.
+__device__ __forceinline__ bool bwd_item(const int32_t* work, const int32_t* row_ptr, int nrow, int most, int H, int* h,
+                                         int* i, int* beg, int* n) {
+    if (work) {
+        const int item = work[blockIdx.x];
+        *h = item >> 16;
+        *i = item & 0xFFFF;
+    } else {
+        *h = static_cast<int>(blockIdx.x) / nrow;
+        *i = static_cast<int>(blockIdx.x) - *h * nrow;
+    }
+    if (*h < 0 || *h >= H || *i >= nrow) {
+        if (threadIdx.x == 0) raise_status(STATUS_BAD_LIST);
+        return false;
+    }
+    *beg = row_ptr[*h * nrow + *i];
+    *n = row_ptr[*h * nrow + *i + 1] - *beg;
+    if (*beg < 0 || *n < 0 || *n > most) {
+        if (threadIdx.x == 0) raise_status(STATUS_BAD_LIST);
+        return false;
+    }
+    return true;
+}
+
+// Shared memory of both kernels: two resident tiles (128 rows of D bf16), two rings of ST tiles of
+// BLK rows, and the row statistics that come with the first ring's tiles.
+template <int D, int BLK, int ST>
+struct BwdSmem {
+    static constexpr int CH = D / 64;                     // 64-column chunks per row
+    static constexpr uint32_t RCHUNK = kTileM * 128;      // chunk of a resident tile
+    static constexpr uint32_t R_BYTES = CH * RCHUNK;
+    static constexpr uint32_t CHUNK = BLK * 128;          // chunk of a ring tile
+    static constexpr uint32_t T_BYTES = CH * CHUNK;
+    static constexpr uint32_t OFF_R0 = 0, OFF_R1 = R_BYTES;
+    static constexpr uint32_t OFF_A = 2 * R_BYTES;        // first ring
+    static constexpr uint32_t OFF_B = OFF_A + ST * T_BYTES;
+    static constexpr uint32_t OFF_ST = OFF_B + ST * T_BYTES;   // float [ST][2][BLK]
+    static constexpr uint32_t OFF_BAR = OFF_ST + ST * 2 * BLK * 4;
+    static constexpr int B_R = 0, B_AF = 1, B_AE = B_AF + ST, B_BF = B_AE + ST, B_BE = B_BF + ST, B_SF = B_BE + ST,
+                         B_SE = B_SF + 1, B_DPF = B_SE + 1, B_PF = B_DPF + 1, B_DSF = B_PF + 1, B_END = B_DSF + 1,
+                         B_DRAIN = B_END + 1, NBARS = B_DRAIN + 1;
+    static constexpr uint32_t OFF_MISC = OFF_BAR + NBARS * 8;
+    // + alignment slack; at least 120 KB, so that one CTA (all 512 TMEM columns) is resident per SM
+    static constexpr uint32_t RAW = OFF_MISC + 16 + 1024;
+    static constexpr uint32_t BYTES = RAW > 120u * 1024 ? RAW : 120u * 1024;
+};
+
+// dK and dV of one key block, over the query blocks that keep it.  With the keys as the rows of
+// every tile,
+//   S^T = K Q^T, dP^T = V dO^T   (K, V resident in shared memory, SS MMAs, M = 128 keys, N = BLK)
+//   P^T = 2^(S^T scale_log2 - LSE), dS^T = P^T (dP^T - delta)
+//   dV += P^T dO, dK += dS^T Q   (TS MMAs: P^T and dS^T from tensor memory, N = D)
+// so both products that reduce over queries take their A operand from tensor memory where the
+// arithmetic left it, and nothing is transposed.  LSE and delta belong to columns and come with
+// each Q tile.  Each sum is complete in one CTA: no atomics, the same bits in every run.
+//
+// Tensor memory is full at D = 128: S [0, BLK), dP [128, 128 + BLK), dV and dK D columns each.  P^T
+// overwrites S and dS^T overwrites dP (each half-row's columns by the warp that loaded them), so
+// the next S waits for dV's product and the next dP for dK's.
+//   warp 0     TMA: K, V once; Q (with its LSE and delta) and dO tiles through two rings.
+//   warp 1     MMA issuer: S, dP of tile 0; then per tile dV, the next S, dK, the next dP.
+//   warps 2..9 arithmetic, two warps per 32 keys, half of a tile's queries each.
+template <int D, int BLK, int ST>
+__global__ void __launch_bounds__(kBwdThreads, 1)
+bwd_kv_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+              const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
+              const __grid_constant__ CUtensorMap tm_qa, const __grid_constant__ CUtensorMap tm_doa, const BwdParams p) {
+    using L = BwdSmem<D, BLK, ST>;
+    constexpr int CH = L::CH, HC = BLK / 2;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    const uint32_t sbase = smem_u32(smem);
+    const uint32_t bar0 = sbase + L::OFF_BAR;
+    auto bar = [&](int idx) -> uint32_t { return bar0 + 8u * idx; };
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::OFF_MISC);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::OFF_MISC + 4);
+    const AttnParams& g = p.geo;
+    const uint32_t warp = warp_id(), lane = lane_id();
+
+    int h, j, beg, n;
+    if (!bwd_item(p.t_work, p.t_row_ptr, g.nk, g.nq, g.H, &h, &j, &beg, &n)) return;
+    const bool rep = repeats(g, h);
+
+    if (threadIdx.x == 0) {
+        mbar_init(bar(L::B_R), 1);
+        for (int s = 0; s < ST; ++s) {
+            mbar_init(bar(L::B_AF + s), 1);
+            mbar_init(bar(L::B_AE + s), 1);
+            mbar_init(bar(L::B_BF + s), 1);
+            mbar_init(bar(L::B_BE + s), 1);
+        }
+        mbar_init(bar(L::B_SF), 1);
+        mbar_init(bar(L::B_DPF), 1);
+        mbar_init(bar(L::B_PF), kBwdArith);
+        mbar_init(bar(L::B_DSF), kBwdArith);
+        mbar_init(bar(L::B_END), 1);
+        mbar_init(bar(L::B_DRAIN), 1);
+        *abort_flag = 0;
+        fence_barrier_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(smem_u32(tmem_slot), kTmemCols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const WaitCtl ctl{abort_flag, p.timeout_ns};
+    int armed_r = 0, armed = 0, armed_b = 0;
+
+    if (n > 0 && warp == 0) {
+        // ===================== TMA producer =============================================
+        const CUtensorMap* mq = rep ? &tm_qa : &tm_q;
+        const CUtensorMap* md = rep ? &tm_doa : &tm_do;
+        if (elect_one()) {
+            mbar_arrive_expect_tx(bar(L::B_R), 2 * L::R_BYTES);
+            for (int c = 0; c < CH; ++c) {
+                tma_load_3d(sbase + L::OFF_R0 + c * L::RCHUNK, &tm_k, bar(L::B_R), c * 64, j * BLK, h);
+                tma_load_3d(sbase + L::OFF_R1 + c * L::RCHUNK, &tm_v, bar(L::B_R), c * 64, j * BLK, h);
+                if (BLK < kTileM) {                        // rows 64..127: a box past the sequence (zeros)
+                    tma_load_3d(sbase + L::OFF_R0 + c * L::RCHUNK + BLK * 128, &tm_k, bar(L::B_R), c * 64, g.N, h);
+                    tma_load_3d(sbase + L::OFF_R1 + c * L::RCHUNK + BLK * 128, &tm_v, bar(L::B_R), c * 64, g.N, h);
                 }
             }
         }
-    }
-    auto put = [&](void* base, size_t at, float y) {
-        if (p.grad_f32) static_cast<float*>(base)[at] = y;
-        else static_cast<__nv_bfloat16*>(base)[at] = __float2bfloat16(y);
-    };
-    if (r >= rows) return;
-    const int tok = !KV && rep ? anchor_token(g, r) : r;
-    const int copies = !KV && rep ? anchor_copies(g, r) : 1;
+        armed_r = 1;
+        const size_t stats = static_cast<size_t>(h) * g.nq * BLK;
+        for (int t = 0; t < n; ++t) {
+            const int s = t % ST;
+            const int i = p.t_col_idx[beg + t];
+            // an index outside the query blocks loads zeros (its P is masked)
+            const int row = i >= 0 && i < g.nq ? i * BLK : g.N;
+            const size_t st_at = stats + (i >= 0 && i < g.nq ? static_cast<size_t>(i) * BLK : 0);
+            if (!mbar_wait_warp(bar(L::B_AE + s), ((t / ST) & 1) ^ 1, ctl)) break;
+            if (elect_one()) {
+                mbar_arrive_expect_tx(bar(L::B_AF + s), L::T_BYTES + 2 * BLK * 4);
+                for (int c = 0; c < CH; ++c)
+                    tma_load_3d(sbase + L::OFF_A + s * L::T_BYTES + c * L::CHUNK, mq, bar(L::B_AF + s), c * 64, row, h);
+                bulk_load(sbase + L::OFF_ST + s * 2 * BLK * 4, p.nlse + st_at, BLK * 4, bar(L::B_AF + s));
+                bulk_load(sbase + L::OFF_ST + (s * 2 + 1) * BLK * 4, p.ndelta + st_at, BLK * 4, bar(L::B_AF + s));
+            }
+            ++armed;
+            if (!mbar_wait_warp(bar(L::B_BE + s), ((t / ST) & 1) ^ 1, ctl)) break;
+            if (elect_one()) {
+                mbar_arrive_expect_tx(bar(L::B_BF + s), L::T_BYTES);
+                for (int c = 0; c < CH; ++c)
+                    tma_load_3d(sbase + L::OFF_B + s * L::T_BYTES + c * L::CHUNK, md, bar(L::B_BF + s), c * 64, row, h);
+            }
+            ++armed_b;
+        }
+    } else if (n > 0 && warp == 1) {
+        // ===================== MMA issuer ===============================================
+        constexpr uint32_t idesc_s = idesc_bf16_f32(kTileM, BLK, false, false);
+        constexpr uint32_t idesc_g = idesc_bf16_f32(kTileM, D, false, true);
+        // dst[keys x queries] = resident (K or V) x ring tile (Q or dO)^T
+        auto scores = [&](uint32_t dst, uint32_t off_r, uint32_t off_t, int s) {
 #pragma unroll
-    for (int y = 0; y < D / 32; ++y) {
-        const size_t at = (static_cast<size_t>(h) * g.N + tok) * D + y * 32 + lane;
-        put(KV ? p.dk : p.dq, at, o1[y] * p.scale);
-        if (KV) put(p.dv, at, o2[y]);
-        // the tokens that only take an anchor's output are no queries of a repeat head
-        for (int c = 1; c < copies; ++c) put(p.dq, at + static_cast<size_t>(c) * g.Wl * D, 0.f);
+            for (int kk = 0; kk < D / 16; ++kk) {
+                const uint64_t ad = smem_desc_sw128(sbase + off_r + (kk >> 2) * L::RCHUNK + (kk & 3) * 32, 16, 1024);
+                const uint64_t bd =
+                    smem_desc_sw128(sbase + off_t + s * L::T_BYTES + (kk >> 2) * L::CHUNK + (kk & 3) * 32, 16, 1024);
+                umma_ss(tmem + dst, ad, bd, idesc_s, kk > 0 ? 1u : 0u);
+            }
+        };
+        // acc[keys x D] += src[keys x queries] (bf16 in TMEM, half hf at column hf * HC) x ring tile
+        auto grads = [&](uint32_t acc, uint32_t src, uint32_t off_t, int s, bool first) {
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+                for (int kk = 0; kk < HC / 16; ++kk) {
+                    const uint64_t bd =
+                        smem_desc_sw128(sbase + off_t + s * L::T_BYTES + (hf * HC + kk * 16) * 128, L::CHUNK, 1024);
+                    umma_ts(tmem + acc, tmem + src + hf * HC + kk * 8, bd, idesc_g, (!first || hf > 0 || kk > 0) ? 1u : 0u);
+                }
+        };
+        bool ok = mbar_wait_warp(bar(L::B_R), 0, ctl);
+        if (ok) ok = mbar_wait_warp(bar(L::B_AF), 0, ctl);
+        if (ok) {
+            tc_fence_after();
+            if (elect_one()) {
+                scores(kBwdTmemS, L::OFF_R0, L::OFF_A, 0);
+                umma_commit(bar(L::B_SF));
+            }
+            ok = mbar_wait_warp(bar(L::B_BF), 0, ctl);
+        }
+        if (ok) {
+            tc_fence_after();
+            if (elect_one()) {
+                scores(kBwdTmemDP, L::OFF_R1, L::OFF_B, 0);
+                umma_commit(bar(L::B_DPF));
+            }
+        }
+        for (int t = 0; ok && t < n; ++t) {
+            const int s = t % ST, ph = (t / ST) & 1, s1 = (t + 1) % ST, ph1 = ((t + 1) / ST) & 1;
+            ok = mbar_wait_warp(bar(L::B_PF), t & 1, ctl);
+            if (!ok) break;
+            tc_fence_after();
+            if (elect_one()) {
+                grads(kBwdTmemAcc, kBwdTmemS, L::OFF_B, s, t == 0);
+                umma_commit(bar(L::B_BE + s));             // dO's stage, and P's columns, are free
+            }
+            if (t + 1 < n) {
+                ok = mbar_wait_warp(bar(L::B_AF + s1), ph1, ctl);
+                if (ok) ok = mbar_wait_warp(bar(L::B_BE + s), ph, ctl);
+                if (!ok) break;
+                tc_fence_after();
+                if (elect_one()) {
+                    scores(kBwdTmemS, L::OFF_R0, L::OFF_A, s1);
+                    umma_commit(bar(L::B_SF));
+                }
+            }
+            ok = mbar_wait_warp(bar(L::B_DSF), t & 1, ctl);
+            if (!ok) break;
+            tc_fence_after();
+            if (elect_one()) {
+                grads(kBwdTmemAcc + D, kBwdTmemDP, L::OFF_A, s, t == 0);
+                umma_commit(bar(L::B_AE + s));
+            }
+            if (t + 1 < n) {
+                ok = mbar_wait_warp(bar(L::B_BF + s1), ph1, ctl);
+                if (ok) ok = mbar_wait_warp(bar(L::B_AE + s), ph, ctl);
+                if (!ok) break;
+                tc_fence_after();
+                if (elect_one()) {
+                    scores(kBwdTmemDP, L::OFF_R1, L::OFF_B, s1);
+                    umma_commit(bar(L::B_DPF));
+                }
+            }
+        }
+        if (ok && elect_one()) umma_commit(bar(L::B_END));
+    } else if (warp >= 2) {
+        // ===================== arithmetic and output ====================================
+        const int hf = static_cast<int>(warp - 2) >> 2;    // half of every tile's queries
+        const uint32_t q4 = warp & 3;
+        const int r = static_cast<int>(q4 * 32 + lane);    // key of the block == TMEM lane
+        const uint32_t lane_base = (q4 * 32) << 16;
+        const float sc = g.scale_log2;
+        const uint32_t ts = tmem + lane_base + kBwdTmemS + hf * HC, td = tmem + lane_base + kBwdTmemDP + hf * HC;
+        bool ok = true;
+        for (int t = 0; t < n; ++t) {
+            const int s = t % ST;
+            const int i = p.t_col_idx[beg + t];
+            const bool live = i >= 0 && i < g.nq;
+            const float* nl = reinterpret_cast<const float*>(smem + L::OFF_ST) + s * 2 * BLK + hf * HC;
+            const float* nd = nl + BLK;
+            ok = mbar_wait_warp(bar(L::B_AF + s), (t / ST) & 1, ctl);     // the statistics, seen by this thread
+            if (ok) ok = mbar_wait_warp(bar(L::B_SF), t & 1, ctl);
+            if (!ok) break;
+            tc_fence_after();
+            float x[HC];
+            tmem_row<HC>(ts, x);
+            uint32_t pk[HC / 2];
+#pragma unroll
+            for (int c = 0; c < HC; c += 4) {
+                const float4 l = *reinterpret_cast<const float4*>(nl + c);
+                ffma2(x[c], x[c + 1], x[c], x[c + 1], sc, sc, l.x, l.y);
+                ffma2(x[c + 2], x[c + 3], x[c + 2], x[c + 3], sc, sc, l.z, l.w);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[c + e] = live ? ex2_approx(x[c + e]) : 0.f;
+                pk[c / 2] = pack_bf16x2(x[c], x[c + 1]);
+                pk[c / 2 + 1] = pack_bf16x2(x[c + 2], x[c + 3]);
+            }
+            tmem_put<HC>(ts, pk);
+            tmem_wait_st();
+            tc_fence_before();
+            mbar_arrive(bar(L::B_PF));
+            ok = mbar_wait_warp(bar(L::B_DPF), t & 1, ctl);
+            if (!ok) break;
+            tc_fence_after();
+            {
+                float y[HC];
+                tmem_row<HC>(td, y);
+#pragma unroll
+                for (int c = 0; c < HC; c += 4) {
+                    const float4 d = *reinterpret_cast<const float4*>(nd + c);
+                    fadd2(y[c], y[c + 1], y[c], y[c + 1], d.x, d.y);
+                    fadd2(y[c + 2], y[c + 3], y[c + 2], y[c + 3], d.z, d.w);
+                    fmul2(y[c], y[c + 1], y[c], y[c + 1], x[c], x[c + 1]);
+                    fmul2(y[c + 2], y[c + 3], y[c + 2], y[c + 3], x[c + 2], x[c + 3]);
+                    pk[c / 2] = pack_bf16x2(y[c], y[c + 1]);
+                    pk[c / 2 + 1] = pack_bf16x2(y[c + 2], y[c + 3]);
+                }
+            }
+            tmem_put<HC>(td, pk);
+            tmem_wait_st();
+            tc_fence_before();
+            mbar_arrive(bar(L::B_DSF));
+        }
+        if (ok && n > 0) ok = mbar_wait_warp(bar(L::B_END), 0, ctl);
+        if (ok) {
+            tc_fence_after();
+            // warps 2..5 write dV, warps 6..9 dK
+            const int tok = j * BLK + r;
+            const bool write = r < BLK && tok < g.N;
+            const size_t at = (static_cast<size_t>(h) * g.N + tok) * D;
+#pragma unroll
+            for (int c = 0; c < D; c += 32)
+                put_grad32(hf ? p.dk : p.dv, at + c, p.grad_f32, tmem + lane_base + kBwdTmemAcc + hf * D + c,
+                           hf ? p.scale : 1.f, n > 0, write);
+        }
+    }
+
+    // ---- teardown (also the abort drain) ----------------------------------------
+    __syncthreads();
+    if (*abort_flag) {
+        constexpr uint64_t kDrainNs = 1000000000ull;
+        if (warp == 0 && lane == 0) {
+            if (armed_r) mbar_wait_drain(bar(L::B_R), 0, kDrainNs);
+            for (int t = max(0, armed - ST); t < armed; ++t) mbar_wait_drain(bar(L::B_AF + t % ST), (t / ST) & 1, kDrainNs);
+            for (int t = max(0, armed_b - ST); t < armed_b; ++t) mbar_wait_drain(bar(L::B_BF + t % ST), (t / ST) & 1, kDrainNs);
+        }
+        if (warp == 1 && lane == 0) {
+            umma_commit(bar(L::B_DRAIN));
+            mbar_wait_drain(bar(L::B_DRAIN), 0, kDrainNs);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, kTmemCols);
+    }
+}
+
+// dQ of one query block, over its kept key blocks:
+//   S = Q K^T, dP = dO V^T   (Q and dO in tensor memory, TS MMAs, M = 128 queries, N = BLK)
+//   dS = 2^(S scale_log2 - LSE) (dP - delta),  dQ += dS K   (TS, N = D)
+// Tensor memory: S [0, BLK), dP [128, 128 + BLK), dQ [256, 256 + D), Q and dO (bf16 pairs) behind it, D / 2
+// columns each.  dS overwrites dP, so the next dP waits for dQ's product; S is handed back as soon as it is
+// loaded, so the next S overlaps this tile's exponentials.  Roles as in bwd_kv_kernel: warp 1 issues S, dP
+// of tile 0 and then per tile the next S, dQ, the next dP.
+template <int D, int BLK, int ST>
+__global__ void __launch_bounds__(kBwdThreads, 1)
+bwd_q_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+             const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
+             const __grid_constant__ CUtensorMap tm_qa, const __grid_constant__ CUtensorMap tm_doa, const BwdParams p) {
+    using L = BwdSmem<D, BLK, ST>;
+    constexpr int CH = L::CH, HC = BLK / 2;
+    constexpr uint32_t TQ = kBwdTmemAcc + D, TDO = TQ + D / 2;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    const uint32_t sbase = smem_u32(smem);
+    const uint32_t bar0 = sbase + L::OFF_BAR;
+    auto bar = [&](int idx) -> uint32_t { return bar0 + 8u * idx; };
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::OFF_MISC);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::OFF_MISC + 4);
+    const AttnParams& g = p.geo;
+    const uint32_t warp = warp_id(), lane = lane_id();
+
+    int h, i, beg, n;
+    if (!bwd_item(p.work, p.row_ptr, g.nq, g.nk, g.H, &h, &i, &beg, &n)) return;
+    const bool rep = repeats(g, h);
+    const int Nq = rep ? g.n_anchor : g.N;
+    if (i * BLK >= Nq) return;                             // rows past the anchor space
+
+    if (threadIdx.x == 0) {
+        mbar_init(bar(L::B_R), 1);
+        for (int s = 0; s < ST; ++s) {
+            mbar_init(bar(L::B_AF + s), 1);
+            mbar_init(bar(L::B_AE + s), 1);
+            mbar_init(bar(L::B_BF + s), 1);
+            mbar_init(bar(L::B_BE + s), 1);
+        }
+        mbar_init(bar(L::B_SF), 1);
+        mbar_init(bar(L::B_SE), kBwdArith);
+        mbar_init(bar(L::B_DPF), 1);
+        mbar_init(bar(L::B_DSF), kBwdArith);
+        mbar_init(bar(L::B_END), 1);
+        mbar_init(bar(L::B_DRAIN), 1);
+        *abort_flag = 0;
+        fence_barrier_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(smem_u32(tmem_slot), kTmemCols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const WaitCtl ctl{abort_flag, p.timeout_ns};
+    int armed_r = 0, armed = 0, armed_b = 0;
+
+    if (n > 0 && warp == 0) {
+        // ===================== TMA producer =============================================
+        const CUtensorMap* mq = rep ? &tm_qa : &tm_q;
+        const CUtensorMap* md = rep ? &tm_doa : &tm_do;
+        if (elect_one()) {
+            mbar_arrive_expect_tx(bar(L::B_R), 2 * L::R_BYTES);
+            for (int c = 0; c < CH; ++c) {
+                tma_load_3d(sbase + L::OFF_R0 + c * L::RCHUNK, mq, bar(L::B_R), c * 64, i * BLK, h);
+                tma_load_3d(sbase + L::OFF_R1 + c * L::RCHUNK, md, bar(L::B_R), c * 64, i * BLK, h);
+                if (BLK < kTileM) {
+                    tma_load_3d(sbase + L::OFF_R0 + c * L::RCHUNK + BLK * 128, mq, bar(L::B_R), c * 64, g.N, h);
+                    tma_load_3d(sbase + L::OFF_R1 + c * L::RCHUNK + BLK * 128, md, bar(L::B_R), c * 64, g.N, h);
+                }
+            }
+        }
+        armed_r = 1;
+        for (int t = 0; t < n; ++t) {
+            const int s = t % ST;
+            const int row = p.col_idx[beg + t] * BLK;
+            if (!mbar_wait_warp(bar(L::B_AE + s), ((t / ST) & 1) ^ 1, ctl)) break;
+            if (elect_one()) {
+                mbar_arrive_expect_tx(bar(L::B_AF + s), L::T_BYTES);
+                for (int c = 0; c < CH; ++c)
+                    tma_load_3d(sbase + L::OFF_A + s * L::T_BYTES + c * L::CHUNK, &tm_k, bar(L::B_AF + s), c * 64, row, h);
+            }
+            ++armed;
+            if (!mbar_wait_warp(bar(L::B_BE + s), ((t / ST) & 1) ^ 1, ctl)) break;
+            if (elect_one()) {
+                mbar_arrive_expect_tx(bar(L::B_BF + s), L::T_BYTES);
+                for (int c = 0; c < CH; ++c)
+                    tma_load_3d(sbase + L::OFF_B + s * L::T_BYTES + c * L::CHUNK, &tm_v, bar(L::B_BF + s), c * 64, row, h);
+            }
+            ++armed_b;
+        }
+    } else if (n > 0 && warp == 1) {
+        // ===================== MMA issuer ===============================================
+        constexpr uint32_t idesc_s = idesc_bf16_f32(kTileM, BLK, false, false);
+        constexpr uint32_t idesc_g = idesc_bf16_f32(kTileM, D, false, true);
+        auto scores = [&](uint32_t dst, uint32_t a, uint32_t off_t, int s) {
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+                const uint64_t bd =
+                    smem_desc_sw128(sbase + off_t + s * L::T_BYTES + (kk >> 2) * L::CHUNK + (kk & 3) * 32, 16, 1024);
+                umma_ts(tmem + dst, tmem + a + kk * 8, bd, idesc_s, kk > 0 ? 1u : 0u);
+            }
+        };
+        bool ok = mbar_wait_warp(bar(L::B_R), 0, ctl);
+        if (ok) {
+            tc_fence_after();
+            if (elect_one()) {
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    tmem_cp_128x256b(tmem + TQ + kk * 8,
+                                     smem_desc_sw128(sbase + L::OFF_R0 + (kk >> 2) * L::RCHUNK + (kk & 3) * 32, 16, 1024));
+                    tmem_cp_128x256b(tmem + TDO + kk * 8,
+                                     smem_desc_sw128(sbase + L::OFF_R1 + (kk >> 2) * L::RCHUNK + (kk & 3) * 32, 16, 1024));
+                }
+            }
+            ok = mbar_wait_warp(bar(L::B_AF), 0, ctl);
+        }
+        if (ok) {
+            tc_fence_after();
+            if (elect_one()) {
+                scores(kBwdTmemS, TQ, L::OFF_A, 0);
+                umma_commit(bar(L::B_SF));
+            }
+            ok = mbar_wait_warp(bar(L::B_BF), 0, ctl);
+        }
+        if (ok) {
+            tc_fence_after();
+            if (elect_one()) {
+                scores(kBwdTmemDP, TDO, L::OFF_B, 0);
+                umma_commit(bar(L::B_DPF));
+                umma_commit(bar(L::B_BE));
+            }
+        }
+        for (int t = 0; ok && t < n; ++t) {
+            const int s = t % ST, ph = (t / ST) & 1, s1 = (t + 1) % ST, ph1 = ((t + 1) / ST) & 1;
+            if (t + 1 < n) {
+                ok = mbar_wait_warp(bar(L::B_AF + s1), ph1, ctl);
+                if (ok) ok = mbar_wait_warp(bar(L::B_SE), t & 1, ctl);
+                if (!ok) break;
+                tc_fence_after();
+                if (elect_one()) {
+                    scores(kBwdTmemS, TQ, L::OFF_A, s1);
+                    umma_commit(bar(L::B_SF));
+                }
+            }
+            ok = mbar_wait_warp(bar(L::B_DSF), t & 1, ctl);
+            if (!ok) break;
+            tc_fence_after();
+            if (elect_one()) {
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+                    for (int kk = 0; kk < HC / 16; ++kk) {
+                        const uint64_t bd = smem_desc_sw128(
+                            sbase + L::OFF_A + s * L::T_BYTES + (hf * HC + kk * 16) * 128, L::CHUNK, 1024);
+                        umma_ts(tmem + kBwdTmemAcc, tmem + kBwdTmemDP + hf * HC + kk * 8, bd, idesc_g,
+                                (t > 0 || hf > 0 || kk > 0) ? 1u : 0u);
+                    }
+                umma_commit(bar(L::B_AE + s));
+            }
+            if (t + 1 < n) {
+                ok = mbar_wait_warp(bar(L::B_BF + s1), ph1, ctl);
+                if (ok) ok = mbar_wait_warp(bar(L::B_AE + s), ph, ctl);   // dS's columns are free
+                if (!ok) break;
+                tc_fence_after();
+                if (elect_one()) {
+                    scores(kBwdTmemDP, TDO, L::OFF_B, s1);
+                    umma_commit(bar(L::B_DPF));
+                    umma_commit(bar(L::B_BE + s1));
+                }
+            }
+        }
+        if (ok && elect_one()) umma_commit(bar(L::B_END));
+    } else if (warp >= 2) {
+        // ===================== arithmetic and output ====================================
+        const int hf = static_cast<int>(warp - 2) >> 2;    // half of every tile's keys
+        const uint32_t q4 = warp & 3;
+        const int r = static_cast<int>(q4 * 32 + lane);    // query of the block == TMEM lane
+        const uint32_t lane_base = (q4 * 32) << 16;
+        const float sc = g.scale_log2;
+        const uint32_t ts = tmem + lane_base + kBwdTmemS + hf * HC, td = tmem + lane_base + kBwdTmemDP + hf * HC;
+        const int qrow = i * BLK + r;
+        const bool row_ok = r < BLK && qrow < Nq;
+        const size_t st_at = static_cast<size_t>(h) * g.nq * BLK + qrow;
+        const float nl = row_ok ? p.nlse[st_at] : -INFINITY, nd = row_ok ? p.ndelta[st_at] : 0.f;
+        bool ok = true;
+        for (int t = 0; t < n; ++t) {
+            const int j = p.col_idx[beg + t];
+            const int valid = (j >= 0 ? min(BLK, g.N - j * BLK) : 0) - hf * HC;
+            ok = mbar_wait_warp(bar(L::B_SF), t & 1, ctl);
+            if (!ok) break;
+            tc_fence_after();
+            float x[HC];
+            tmem_row<HC>(ts, x);
+            tc_fence_before();
+            mbar_arrive(bar(L::B_SE));                     // S may be overwritten by the next one
+#pragma unroll
+            for (int c = 0; c < HC; c += 2) {
+                ffma2(x[c], x[c + 1], x[c], x[c + 1], sc, sc, nl, nl);
+                x[c] = ex2_approx(x[c]);
+                x[c + 1] = ex2_approx(x[c + 1]);
+            }
+            if (valid < HC) {                              // ragged last key block only
+#pragma unroll
+                for (int c = 0; c < HC; ++c)
+                    if (c >= valid) x[c] = 0.f;
+            }
+            ok = mbar_wait_warp(bar(L::B_DPF), t & 1, ctl);
+            if (!ok) break;
+            tc_fence_after();
+            uint32_t pk[HC / 2];
+            {
+                float y[HC];
+                tmem_row<HC>(td, y);
+#pragma unroll
+                for (int c = 0; c < HC; c += 2) {
+                    fadd2(y[c], y[c + 1], y[c], y[c + 1], nd, nd);
+                    fmul2(y[c], y[c + 1], y[c], y[c + 1], x[c], x[c + 1]);
+                    pk[c / 2] = pack_bf16x2(y[c], y[c + 1]);
+                }
+            }
+            tmem_put<HC>(td, pk);
+            tmem_wait_st();
+            tc_fence_before();
+            mbar_arrive(bar(L::B_DSF));
+        }
+        if (ok && n > 0) ok = mbar_wait_warp(bar(L::B_END), 0, ctl);
+        if (ok) {
+            tc_fence_after();
+            const int tok = rep && row_ok ? anchor_token(g, qrow) : qrow;
+            const int copies = rep && row_ok ? anchor_copies(g, qrow) : 1;
+            const size_t at = (static_cast<size_t>(h) * g.N + tok) * D;
+#pragma unroll
+            for (int c = hf * (D / 2); c < (hf + 1) * (D / 2); c += 32) {
+                put_grad32(p.dq, at + c, p.grad_f32, tmem + lane_base + kBwdTmemAcc + c, p.scale, n > 0, row_ok);
+                // the tokens that only take an anchor's output are no queries of a repeat head
+                for (int y = 1; y < copies; ++y)
+                    put_grad32(p.dq, at + static_cast<size_t>(y) * g.Wl * D + c, p.grad_f32, 0u, 0.f, false, true);
+            }
+        }
+    }
+
+    // ---- teardown (also the abort drain) ----------------------------------------
+    __syncthreads();
+    if (*abort_flag) {
+        constexpr uint64_t kDrainNs = 1000000000ull;
+        if (warp == 0 && lane == 0) {
+            if (armed_r) mbar_wait_drain(bar(L::B_R), 0, kDrainNs);
+            for (int t = max(0, armed - ST); t < armed; ++t) mbar_wait_drain(bar(L::B_AF + t % ST), (t / ST) & 1, kDrainNs);
+            for (int t = max(0, armed_b - ST); t < armed_b; ++t) mbar_wait_drain(bar(L::B_BF + t % ST), (t / ST) & 1, kDrainNs);
+        }
+        if (warp == 1 && lane == 0) {
+            umma_commit(bar(L::B_DRAIN));
+            mbar_wait_drain(bar(L::B_DRAIN), 0, kDrainNs);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, kTmemCols);
     }
 }
 

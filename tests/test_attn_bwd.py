@@ -209,8 +209,11 @@ def _bounds(q, k, v, o, do, lse, scale, B, mask, u_do):
     e = (D + 8) * U32 * size.max(initial=0.0) + max(N, Nq) * U32 + 2.0 ** -20
     d32 = (D + 8) * U32 * (np.abs(do) @ np.abs(v).T + (np.abs(do) * np.abs(o)).sum(1)[:, None])
     d = d32 + u_do * (np.abs(do) @ np.abs(v).T)
-    aS = (U16 + e) * np.abs(dS) + P * d
-    most = (scale * aS @ np.abs(k), scale * aS.T @ np.abs(q), (U16 + e + u_do) * P.T @ np.abs(do))
+    # what is below the smallest normal number, 2^-126, may become 0: each P loses that much at most, and each dS
+    # that times |dP - delta| and once more for its own size
+    least = 2.0 ** -126 * keep
+    aS = (U16 + e) * np.abs(dS) + P * d + least * (1 + np.abs(dP - delta[:, None]))
+    most = (scale * aS @ np.abs(k), scale * aS.T @ np.abs(q), ((U16 + e + u_do) * P + least).T @ np.abs(do))
     # d32 counts too: where dP - delta cancels (one key: P = 1 and o = v, dS is 0 exactly) it is all there is
     sq = (U16 ** 2 / 3 + e ** 2) * dS ** 2 + (P * d32) ** 2 + P ** 2 * (u_do ** 2 / 3 * (do ** 2 @ (v ** 2).T))
     mean = (scale ** 2 * sq @ k ** 2, scale ** 2 * sq.T @ q ** 2,
