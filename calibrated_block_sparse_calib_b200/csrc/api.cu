@@ -322,26 +322,19 @@ BwdSpace bwd_space(int H, int N, int D, int B, long long n_anchor, bool io_f32) 
     return w;
 }
 
-struct BwdMaps {
-    CUtensorMap k, v, q, dout, qa, doa;
-};
-
 template <int D, int BLK>
-calib_status launch_bwd(const BwdMaps& m, const calib::BwdParams& p, cudaStream_t st) {
-    constexpr int ST = 2;   // ring depth (with the two resident tiles, 194 KB at D = B = 128)
+calib_status launch_bwd(const calib::BwdMaps& m, const calib::BwdParams& p, cudaStream_t st) {
+    // ring depth: what fits beside the two resident tiles (194 KB at D = B = 128, at most 194 KB elsewhere)
+    constexpr int ST = D == 128 && BLK == 128 ? 2 : 4;
     using L = calib::BwdSmem<D, BLK, ST>;
     static_assert(L::BYTES <= 232448, "shared memory budget");
     const int rows = p.geo.nq * BLK;
     const long long threads = static_cast<long long>(p.geo.H) * rows * (D / 8);
-    auto* fq = calib::bwd_q_kernel<D, BLK, ST>;
-    auto* fkv = calib::bwd_kv_kernel<D, BLK, ST>;
-    if (calib_status s = ensure_smem(reinterpret_cast<const void*>(fq), L::BYTES)) return s;
-    if (calib_status s = ensure_smem(reinterpret_cast<const void*>(fkv), L::BYTES)) return s;
+    auto* fn = calib::bwd_kernel<D, BLK, ST>;
+    if (calib_status s = ensure_smem(reinterpret_cast<const void*>(fn), L::BYTES)) return s;
     calib::bwd_prepare_kernel<D><<<static_cast<int>((threads + 255) / 256), 256, 0, st>>>(p, rows);
     if (calib_status s = launch_status()) return s;
-    fkv<<<p.geo.H * p.geo.nk, calib::kBwdThreads, L::BYTES, st>>>(m.k, m.v, m.q, m.dout, m.qa, m.doa, p);
-    if (calib_status s = launch_status()) return s;
-    fq<<<p.geo.H * p.geo.nq, calib::kBwdThreads, L::BYTES, st>>>(m.k, m.v, m.q, m.dout, m.qa, m.doa, p);
+    fn<<<p.geo.H * (p.geo.nk + p.geo.nq), calib::kBwdThreads, L::BYTES, st>>>(m, p);
     return launch_status();
 }
 
@@ -389,7 +382,7 @@ calib_status bwd_common(const void* q, const void* k, const void* v, const void*
     p.scale = scale;
     p.grad_f32 = (flags & CALIB_ATTN_GRAD_F32) ? 1 : 0;
     p.timeout_ns = kDefaultTimeoutNs;
-    BwdMaps m;
+    calib::BwdMaps m;
     m.k = c.tk;
     m.v = c.tv;
     m.q = c.tq;

@@ -6,6 +6,11 @@
 
 namespace calib {
 
+// K, V; Q and dO by token; Q and dO by anchor (repeat heads).
+struct BwdMaps {
+    CUtensorMap k, v, q, dout, qa, doa;
+};
+
 struct BwdParams {
     const __nv_bfloat16 *q, *k, *v;      // [H, N, D]
     const void *o, *dout;                // [H, N, D] bf16, or fp32 when io_f32
@@ -109,9 +114,22 @@ __global__ void __launch_bounds__(256) bwd_prepare_kernel(const BwdParams p, int
 
 constexpr int kBwdThreads = 320;          // warp 0 TMA, warp 1 MMA, warps 2..9 arithmetic
 constexpr int kBwdArith = 256;
-constexpr uint32_t kBwdTmemS = 0;         // S (fp32, BLK columns)
-constexpr uint32_t kBwdTmemDP = 128;      // dP (fp32, BLK columns)
-constexpr uint32_t kBwdTmemAcc = 256;     // the accumulators, D columns each
+
+// Tensor-memory columns: S and dP (fp32, BLK columns each), P and dS (bf16 pairs, BLK / 2 each), the
+// accumulators (D each) and, for dQ, Q and dO (bf16 pairs, D / 2 each).  All of it fits 512 columns except
+// at D = BLK = 128; there P overwrites S and dS overwrites dP, each half-row's columns by the warp that
+// loaded them, and the next S (dP) waits for the product that reads P (dS).  HALF: columns between the two
+// halves of P or dS.
+template <int D, int BLK>
+struct BwdTmem {
+    static constexpr bool SEP = 3 * BLK + 2 * D <= 512;
+    static constexpr uint32_t S = 0, DP = BLK;
+    static constexpr uint32_t P = SEP ? 2 * BLK : S, HALF = SEP ? BLK / 4 : BLK / 2;
+    static constexpr uint32_t DS = SEP ? 2 * BLK + BLK / 2 : DP;
+    static constexpr uint32_t ACC = SEP ? 3 * BLK : 2 * BLK;
+    static constexpr uint32_t Q = ACC + D, DO = Q + D / 2;
+    static_assert(ACC + 2 * D <= 512, "tensor memory");
+};
 
 // (d0, d1) = (a0, a1) * (b0, b1), packed fp32x2
 __device__ __forceinline__ void fmul2(float& d0, float& d1, float a0, float a1, float b0, float b1) {
@@ -164,16 +182,16 @@ __device__ __forceinline__ void put_grad32(void* base, size_t at, bool f32, uint
     }
 }
 
-// The work item of a CTA: head, block, and its list row.  False: nothing to write.
-__device__ __forceinline__ bool bwd_item(const int32_t* work, const int32_t* row_ptr, int nrow, int most, int H, int* h,
-                                         int* i, int* beg, int* n) {
+// Work item `id`: head, block, and its list row.  False: nothing to write.
+__device__ __forceinline__ bool bwd_item(int id, const int32_t* work, const int32_t* row_ptr, int nrow, int most, int H,
+                                         int* h, int* i, int* beg, int* n) {
     if (work) {
-        const int item = work[blockIdx.x];
+        const int item = work[id];
         *h = item >> 16;
         *i = item & 0xFFFF;
     } else {
-        *h = static_cast<int>(blockIdx.x) / nrow;
-        *i = static_cast<int>(blockIdx.x) - *h * nrow;
+        *h = id / nrow;
+        *i = id - *h * nrow;
     }
     if (*h < 0 || *h >= H || *i >= nrow) {
         if (threadIdx.x == 0) raise_status(STATUS_BAD_LIST);
@@ -203,7 +221,7 @@ struct BwdSmem {
     static constexpr uint32_t OFF_ST = OFF_B + ST * T_BYTES;   // float [ST][2][BLK]
     static constexpr uint32_t OFF_BAR = OFF_ST + ST * 2 * BLK * 4;
     static constexpr int B_R = 0, B_AF = 1, B_AE = B_AF + ST, B_BF = B_AE + ST, B_BE = B_BF + ST, B_SF = B_BE + ST,
-                         B_SE = B_SF + 1, B_DPF = B_SE + 1, B_PF = B_DPF + 1, B_DSF = B_PF + 1, B_END = B_DSF + 1,
+                         B_SE = B_SF + 1, B_DPF = B_SE + 1, B_DPE = B_DPF + 1, B_PF = B_DPE + 1, B_DSF = B_PF + 1, B_END = B_DSF + 1,
                          B_DRAIN = B_END + 1, NBARS = B_DRAIN + 1;
     static constexpr uint32_t OFF_MISC = OFF_BAR + NBARS * 8;
     // + alignment slack; at least 120 KB, so that one CTA (all 512 TMEM columns) is resident per SM
@@ -220,18 +238,14 @@ struct BwdSmem {
 // arithmetic left it, and nothing is transposed.  LSE and delta belong to columns and come with
 // each Q tile.  Each sum is complete in one CTA: no atomics, the same bits in every run.
 //
-// Tensor memory is full at D = 128: S [0, BLK), dP [128, 128 + BLK), dV and dK D columns each.  P^T
-// overwrites S and dS^T overwrites dP (each half-row's columns by the warp that loaded them), so
-// the next S waits for dV's product and the next dP for dK's.
 //   warp 0     TMA: K, V once; Q (with its LSE and delta) and dO tiles through two rings.
-//   warp 1     MMA issuer: S, dP of tile 0; then per tile dV, the next S, dK, the next dP.
+//   warp 1     MMA issuer: S, dP of tile 0; then per tile the next S, dV, the next dP, dK (dV, the next S, dK, the
+//              next dP where P and dS share columns with S and dP).
 //   warps 2..9 arithmetic, two warps per 32 keys, half of a tile's queries each.
 template <int D, int BLK, int ST>
-__global__ void __launch_bounds__(kBwdThreads, 1)
-bwd_kv_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-              const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
-              const __grid_constant__ CUtensorMap tm_qa, const __grid_constant__ CUtensorMap tm_doa, const BwdParams p) {
+__device__ __forceinline__ void bwd_kv(const BwdMaps& m, const BwdParams& p, int id) {
     using L = BwdSmem<D, BLK, ST>;
+    using T = BwdTmem<D, BLK>;
     constexpr int CH = L::CH, HC = BLK / 2;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -244,7 +258,7 @@ bwd_kv_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
     const uint32_t warp = warp_id(), lane = lane_id();
 
     int h, j, beg, n;
-    if (!bwd_item(p.t_work, p.t_row_ptr, g.nk, g.nq, g.H, &h, &j, &beg, &n)) return;
+    if (!bwd_item(id, p.t_work, p.t_row_ptr, g.nk, g.nq, g.H, &h, &j, &beg, &n)) return;
     const bool rep = repeats(g, h);
 
     if (threadIdx.x == 0) {
@@ -256,7 +270,9 @@ bwd_kv_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
             mbar_init(bar(L::B_BE + s), 1);
         }
         mbar_init(bar(L::B_SF), 1);
+        mbar_init(bar(L::B_SE), kBwdArith);
         mbar_init(bar(L::B_DPF), 1);
+        mbar_init(bar(L::B_DPE), kBwdArith);
         mbar_init(bar(L::B_PF), kBwdArith);
         mbar_init(bar(L::B_DSF), kBwdArith);
         mbar_init(bar(L::B_END), 1);
@@ -277,16 +293,16 @@ bwd_kv_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
 
     if (n > 0 && warp == 0) {
         // ===================== TMA producer =============================================
-        const CUtensorMap* mq = rep ? &tm_qa : &tm_q;
-        const CUtensorMap* md = rep ? &tm_doa : &tm_do;
+        const CUtensorMap* mq = rep ? &m.qa : &m.q;
+        const CUtensorMap* md = rep ? &m.doa : &m.dout;
         if (elect_one()) {
             mbar_arrive_expect_tx(bar(L::B_R), 2 * L::R_BYTES);
             for (int c = 0; c < CH; ++c) {
-                tma_load_3d(sbase + L::OFF_R0 + c * L::RCHUNK, &tm_k, bar(L::B_R), c * 64, j * BLK, h);
-                tma_load_3d(sbase + L::OFF_R1 + c * L::RCHUNK, &tm_v, bar(L::B_R), c * 64, j * BLK, h);
+                tma_load_3d(sbase + L::OFF_R0 + c * L::RCHUNK, &m.k, bar(L::B_R), c * 64, j * BLK, h);
+                tma_load_3d(sbase + L::OFF_R1 + c * L::RCHUNK, &m.v, bar(L::B_R), c * 64, j * BLK, h);
                 if (BLK < kTileM) {                        // rows 64..127: a box past the sequence (zeros)
-                    tma_load_3d(sbase + L::OFF_R0 + c * L::RCHUNK + BLK * 128, &tm_k, bar(L::B_R), c * 64, g.N, h);
-                    tma_load_3d(sbase + L::OFF_R1 + c * L::RCHUNK + BLK * 128, &tm_v, bar(L::B_R), c * 64, g.N, h);
+                    tma_load_3d(sbase + L::OFF_R0 + c * L::RCHUNK + BLK * 128, &m.k, bar(L::B_R), c * 64, g.N, h);
+                    tma_load_3d(sbase + L::OFF_R1 + c * L::RCHUNK + BLK * 128, &m.v, bar(L::B_R), c * 64, g.N, h);
                 }
             }
         }
@@ -329,7 +345,7 @@ bwd_kv_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
                 umma_ss(tmem + dst, ad, bd, idesc_s, kk > 0 ? 1u : 0u);
             }
         };
-        // acc[keys x D] += src[keys x queries] (bf16 in TMEM, half hf at column hf * HC) x ring tile
+        // acc[keys x D] += src[keys x queries] (bf16 in TMEM) x ring tile
         auto grads = [&](uint32_t acc, uint32_t src, uint32_t off_t, int s, bool first) {
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf)
@@ -337,7 +353,7 @@ bwd_kv_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
                 for (int kk = 0; kk < HC / 16; ++kk) {
                     const uint64_t bd =
                         smem_desc_sw128(sbase + off_t + s * L::T_BYTES + (hf * HC + kk * 16) * 128, L::CHUNK, 1024);
-                    umma_ts(tmem + acc, tmem + src + hf * HC + kk * 8, bd, idesc_g, (!first || hf > 0 || kk > 0) ? 1u : 0u);
+                    umma_ts(tmem + acc, tmem + src + hf * T::HALF + kk * 8, bd, idesc_g, (!first || hf > 0 || kk > 0) ? 1u : 0u);
                 }
         };
         bool ok = mbar_wait_warp(bar(L::B_R), 0, ctl);
@@ -345,7 +361,7 @@ bwd_kv_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
         if (ok) {
             tc_fence_after();
             if (elect_one()) {
-                scores(kBwdTmemS, L::OFF_R0, L::OFF_A, 0);
+                scores(T::S, L::OFF_R0, L::OFF_A, 0);
                 umma_commit(bar(L::B_SF));
             }
             ok = mbar_wait_warp(bar(L::B_BF), 0, ctl);
@@ -353,46 +369,57 @@ bwd_kv_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
         if (ok) {
             tc_fence_after();
             if (elect_one()) {
-                scores(kBwdTmemDP, L::OFF_R1, L::OFF_B, 0);
+                scores(T::DP, L::OFF_R1, L::OFF_B, 0);
                 umma_commit(bar(L::B_DPF));
             }
         }
+        // the next tile's S, once the previous one has been loaded (SEP) or P's product is done with its columns
+        auto next_s = [&](int t) -> bool {
+            const int s = t % ST, s1 = (t + 1) % ST;
+            bool r = mbar_wait_warp(bar(L::B_AF + s1), ((t + 1) / ST) & 1, ctl);
+            if (r) r = T::SEP ? mbar_wait_warp(bar(L::B_SE), t & 1, ctl) : mbar_wait_warp(bar(L::B_BE + s), (t / ST) & 1, ctl);
+            if (!r) return false;
+            tc_fence_after();
+            if (elect_one()) {
+                scores(T::S, L::OFF_R0, L::OFF_A, s1);
+                umma_commit(bar(L::B_SF));
+            }
+            return true;
+        };
+        // the next dP, once the previous one has been loaded (SEP) or dS's product is done with its columns
+        auto next_dp = [&](int t) -> bool {
+            const int s = t % ST, s1 = (t + 1) % ST;
+            bool r = mbar_wait_warp(bar(L::B_BF + s1), ((t + 1) / ST) & 1, ctl);
+            if (r) r = T::SEP ? mbar_wait_warp(bar(L::B_DPE), t & 1, ctl) : mbar_wait_warp(bar(L::B_AE + s), (t / ST) & 1, ctl);
+            if (!r) return false;
+            tc_fence_after();
+            if (elect_one()) {
+                scores(T::DP, L::OFF_R1, L::OFF_B, s1);
+                umma_commit(bar(L::B_DPF));
+            }
+            return true;
+        };
         for (int t = 0; ok && t < n; ++t) {
-            const int s = t % ST, ph = (t / ST) & 1, s1 = (t + 1) % ST, ph1 = ((t + 1) / ST) & 1;
+            const int s = t % ST;
+            const bool more = t + 1 < n;
+            if (T::SEP && more && !(ok = next_s(t))) break;
             ok = mbar_wait_warp(bar(L::B_PF), t & 1, ctl);
             if (!ok) break;
             tc_fence_after();
             if (elect_one()) {
-                grads(kBwdTmemAcc, kBwdTmemS, L::OFF_B, s, t == 0);
+                grads(T::ACC, T::P, L::OFF_B, s, t == 0);
                 umma_commit(bar(L::B_BE + s));             // dO's stage, and P's columns, are free
             }
-            if (t + 1 < n) {
-                ok = mbar_wait_warp(bar(L::B_AF + s1), ph1, ctl);
-                if (ok) ok = mbar_wait_warp(bar(L::B_BE + s), ph, ctl);
-                if (!ok) break;
-                tc_fence_after();
-                if (elect_one()) {
-                    scores(kBwdTmemS, L::OFF_R0, L::OFF_A, s1);
-                    umma_commit(bar(L::B_SF));
-                }
-            }
+            if (!T::SEP && more && !(ok = next_s(t))) break;
+            if (T::SEP && more && !(ok = next_dp(t))) break;
             ok = mbar_wait_warp(bar(L::B_DSF), t & 1, ctl);
             if (!ok) break;
             tc_fence_after();
             if (elect_one()) {
-                grads(kBwdTmemAcc + D, kBwdTmemDP, L::OFF_A, s, t == 0);
-                umma_commit(bar(L::B_AE + s));
+                grads(T::ACC + D, T::DS, L::OFF_A, s, t == 0);
+                umma_commit(bar(L::B_AE + s));             // Q's stage, and dS's columns, are free
             }
-            if (t + 1 < n) {
-                ok = mbar_wait_warp(bar(L::B_BF + s1), ph1, ctl);
-                if (ok) ok = mbar_wait_warp(bar(L::B_AE + s), ph, ctl);
-                if (!ok) break;
-                tc_fence_after();
-                if (elect_one()) {
-                    scores(kBwdTmemDP, L::OFF_R1, L::OFF_B, s1);
-                    umma_commit(bar(L::B_DPF));
-                }
-            }
+            if (!T::SEP && more && !(ok = next_dp(t))) break;
         }
         if (ok && elect_one()) umma_commit(bar(L::B_END));
     } else if (warp >= 2) {
@@ -402,7 +429,7 @@ bwd_kv_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
         const int r = static_cast<int>(q4 * 32 + lane);    // key of the block == TMEM lane
         const uint32_t lane_base = (q4 * 32) << 16;
         const float sc = g.scale_log2;
-        const uint32_t ts = tmem + lane_base + kBwdTmemS + hf * HC, td = tmem + lane_base + kBwdTmemDP + hf * HC;
+        const uint32_t ts = tmem + lane_base + T::S + hf * HC, td = tmem + lane_base + T::DP + hf * HC;
         bool ok = true;
         for (int t = 0; t < n; ++t) {
             const int s = t % ST;
@@ -416,6 +443,10 @@ bwd_kv_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
             tc_fence_after();
             float x[HC];
             tmem_row<HC>(ts, x);
+            if constexpr (T::SEP) {
+                tc_fence_before();
+                mbar_arrive(bar(L::B_SE));                 // S may be overwritten by the next one
+            }
             uint32_t pk[HC / 2];
 #pragma unroll
             for (int c = 0; c < HC; c += 4) {
@@ -427,7 +458,9 @@ bwd_kv_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
                 pk[c / 2] = pack_bf16x2(x[c], x[c + 1]);
                 pk[c / 2 + 1] = pack_bf16x2(x[c + 2], x[c + 3]);
             }
-            tmem_put<HC>(ts, pk);
+            // the previous P has been read by its product
+            if (T::SEP && t > 0 && !(ok = mbar_wait_warp(bar(L::B_BE + (t - 1) % ST), ((t - 1) / ST) & 1, ctl))) break;
+            tmem_put<HC>(tmem + lane_base + T::P + hf * T::HALF, pk);
             tmem_wait_st();
             tc_fence_before();
             mbar_arrive(bar(L::B_PF));
@@ -437,6 +470,10 @@ bwd_kv_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
             {
                 float y[HC];
                 tmem_row<HC>(td, y);
+                if constexpr (T::SEP) {
+                    tc_fence_before();
+                    mbar_arrive(bar(L::B_DPE));            // dP may be overwritten by the next one
+                }
 #pragma unroll
                 for (int c = 0; c < HC; c += 4) {
                     const float4 d = *reinterpret_cast<const float4*>(nd + c);
@@ -448,7 +485,9 @@ bwd_kv_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
                     pk[c / 2 + 1] = pack_bf16x2(y[c + 2], y[c + 3]);
                 }
             }
-            tmem_put<HC>(td, pk);
+            // the previous dS has been read by its product
+            if (T::SEP && t > 0 && !(ok = mbar_wait_warp(bar(L::B_AE + (t - 1) % ST), ((t - 1) / ST) & 1, ctl))) break;
+            tmem_put<HC>(tmem + lane_base + T::DS + hf * T::HALF, pk);
             tmem_wait_st();
             tc_fence_before();
             mbar_arrive(bar(L::B_DSF));
@@ -462,7 +501,7 @@ bwd_kv_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
             const size_t at = (static_cast<size_t>(h) * g.N + tok) * D;
 #pragma unroll
             for (int c = 0; c < D; c += 32)
-                put_grad32(hf ? p.dk : p.dv, at + c, p.grad_f32, tmem + lane_base + kBwdTmemAcc + hf * D + c,
+                put_grad32(hf ? p.dk : p.dv, at + c, p.grad_f32, tmem + lane_base + T::ACC + hf * D + c,
                            hf ? p.scale : 1.f, n > 0, write);
         }
     }
@@ -492,18 +531,14 @@ bwd_kv_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
 // dQ of one query block, over its kept key blocks:
 //   S = Q K^T, dP = dO V^T   (Q and dO in tensor memory, TS MMAs, M = 128 queries, N = BLK)
 //   dS = 2^(S scale_log2 - LSE) (dP - delta),  dQ += dS K   (TS, N = D)
-// Tensor memory: S [0, BLK), dP [128, 128 + BLK), dQ [256, 256 + D), Q and dO (bf16 pairs) behind it, D / 2
-// columns each.  dS overwrites dP, so the next dP waits for dQ's product; S is handed back as soon as it is
-// loaded, so the next S overlaps this tile's exponentials.  Roles as in bwd_kv_kernel: warp 1 issues S, dP
-// of tile 0 and then per tile the next S, dQ, the next dP.
+// S is handed back as soon as it is loaded, so the next S overlaps this tile's exponentials.  Roles as in
+// bwd_kv: warp 1 issues S, dP of tile 0 and then per tile the next S, the next dP, dQ (dQ before the next dP where
+// dS shares columns with dP).
 template <int D, int BLK, int ST>
-__global__ void __launch_bounds__(kBwdThreads, 1)
-bwd_q_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-             const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
-             const __grid_constant__ CUtensorMap tm_qa, const __grid_constant__ CUtensorMap tm_doa, const BwdParams p) {
+__device__ __forceinline__ void bwd_q(const BwdMaps& m, const BwdParams& p, int id) {
     using L = BwdSmem<D, BLK, ST>;
+    using T = BwdTmem<D, BLK>;
     constexpr int CH = L::CH, HC = BLK / 2;
-    constexpr uint32_t TQ = kBwdTmemAcc + D, TDO = TQ + D / 2;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     const uint32_t sbase = smem_u32(smem);
@@ -515,7 +550,7 @@ bwd_q_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
     const uint32_t warp = warp_id(), lane = lane_id();
 
     int h, i, beg, n;
-    if (!bwd_item(p.work, p.row_ptr, g.nq, g.nk, g.H, &h, &i, &beg, &n)) return;
+    if (!bwd_item(id, p.work, p.row_ptr, g.nq, g.nk, g.H, &h, &i, &beg, &n)) return;
     const bool rep = repeats(g, h);
     const int Nq = rep ? g.n_anchor : g.N;
     if (i * BLK >= Nq) return;                             // rows past the anchor space
@@ -531,6 +566,7 @@ bwd_q_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
         mbar_init(bar(L::B_SF), 1);
         mbar_init(bar(L::B_SE), kBwdArith);
         mbar_init(bar(L::B_DPF), 1);
+        mbar_init(bar(L::B_DPE), kBwdArith);
         mbar_init(bar(L::B_DSF), kBwdArith);
         mbar_init(bar(L::B_END), 1);
         mbar_init(bar(L::B_DRAIN), 1);
@@ -550,8 +586,8 @@ bwd_q_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
 
     if (n > 0 && warp == 0) {
         // ===================== TMA producer =============================================
-        const CUtensorMap* mq = rep ? &tm_qa : &tm_q;
-        const CUtensorMap* md = rep ? &tm_doa : &tm_do;
+        const CUtensorMap* mq = rep ? &m.qa : &m.q;
+        const CUtensorMap* md = rep ? &m.doa : &m.dout;
         if (elect_one()) {
             mbar_arrive_expect_tx(bar(L::B_R), 2 * L::R_BYTES);
             for (int c = 0; c < CH; ++c) {
@@ -571,14 +607,14 @@ bwd_q_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
             if (elect_one()) {
                 mbar_arrive_expect_tx(bar(L::B_AF + s), L::T_BYTES);
                 for (int c = 0; c < CH; ++c)
-                    tma_load_3d(sbase + L::OFF_A + s * L::T_BYTES + c * L::CHUNK, &tm_k, bar(L::B_AF + s), c * 64, row, h);
+                    tma_load_3d(sbase + L::OFF_A + s * L::T_BYTES + c * L::CHUNK, &m.k, bar(L::B_AF + s), c * 64, row, h);
             }
             ++armed;
             if (!mbar_wait_warp(bar(L::B_BE + s), ((t / ST) & 1) ^ 1, ctl)) break;
             if (elect_one()) {
                 mbar_arrive_expect_tx(bar(L::B_BF + s), L::T_BYTES);
                 for (int c = 0; c < CH; ++c)
-                    tma_load_3d(sbase + L::OFF_B + s * L::T_BYTES + c * L::CHUNK, &tm_v, bar(L::B_BF + s), c * 64, row, h);
+                    tma_load_3d(sbase + L::OFF_B + s * L::T_BYTES + c * L::CHUNK, &m.v, bar(L::B_BF + s), c * 64, row, h);
             }
             ++armed_b;
         }
@@ -600,9 +636,9 @@ bwd_q_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
             if (elect_one()) {
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk) {
-                    tmem_cp_128x256b(tmem + TQ + kk * 8,
+                    tmem_cp_128x256b(tmem + T::Q + kk * 8,
                                      smem_desc_sw128(sbase + L::OFF_R0 + (kk >> 2) * L::RCHUNK + (kk & 3) * 32, 16, 1024));
-                    tmem_cp_128x256b(tmem + TDO + kk * 8,
+                    tmem_cp_128x256b(tmem + T::DO + kk * 8,
                                      smem_desc_sw128(sbase + L::OFF_R1 + (kk >> 2) * L::RCHUNK + (kk & 3) * 32, 16, 1024));
                 }
             }
@@ -611,7 +647,7 @@ bwd_q_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
         if (ok) {
             tc_fence_after();
             if (elect_one()) {
-                scores(kBwdTmemS, TQ, L::OFF_A, 0);
+                scores(T::S, T::Q, L::OFF_A, 0);
                 umma_commit(bar(L::B_SF));
             }
             ok = mbar_wait_warp(bar(L::B_BF), 0, ctl);
@@ -619,22 +655,38 @@ bwd_q_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
         if (ok) {
             tc_fence_after();
             if (elect_one()) {
-                scores(kBwdTmemDP, TDO, L::OFF_B, 0);
+                scores(T::DP, T::DO, L::OFF_B, 0);
                 umma_commit(bar(L::B_DPF));
                 umma_commit(bar(L::B_BE));
             }
         }
+        // the next dP, once the previous one has been loaded (SEP) or dS's product is done with its columns
+        auto next_dp = [&](int t) -> bool {
+            const int s = t % ST, s1 = (t + 1) % ST;
+            bool r = mbar_wait_warp(bar(L::B_BF + s1), ((t + 1) / ST) & 1, ctl);
+            if (r) r = T::SEP ? mbar_wait_warp(bar(L::B_DPE), t & 1, ctl) : mbar_wait_warp(bar(L::B_AE + s), (t / ST) & 1, ctl);
+            if (!r) return false;
+            tc_fence_after();
+            if (elect_one()) {
+                scores(T::DP, T::DO, L::OFF_B, s1);
+                umma_commit(bar(L::B_DPF));
+                umma_commit(bar(L::B_BE + s1));
+            }
+            return true;
+        };
         for (int t = 0; ok && t < n; ++t) {
-            const int s = t % ST, ph = (t / ST) & 1, s1 = (t + 1) % ST, ph1 = ((t + 1) / ST) & 1;
-            if (t + 1 < n) {
-                ok = mbar_wait_warp(bar(L::B_AF + s1), ph1, ctl);
+            const int s = t % ST, s1 = (t + 1) % ST;
+            const bool more = t + 1 < n;
+            if (more) {
+                ok = mbar_wait_warp(bar(L::B_AF + s1), ((t + 1) / ST) & 1, ctl);
                 if (ok) ok = mbar_wait_warp(bar(L::B_SE), t & 1, ctl);
                 if (!ok) break;
                 tc_fence_after();
                 if (elect_one()) {
-                    scores(kBwdTmemS, TQ, L::OFF_A, s1);
+                    scores(T::S, T::Q, L::OFF_A, s1);
                     umma_commit(bar(L::B_SF));
                 }
+                if (T::SEP && !(ok = next_dp(t))) break;
             }
             ok = mbar_wait_warp(bar(L::B_DSF), t & 1, ctl);
             if (!ok) break;
@@ -646,22 +698,12 @@ bwd_q_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
                     for (int kk = 0; kk < HC / 16; ++kk) {
                         const uint64_t bd = smem_desc_sw128(
                             sbase + L::OFF_A + s * L::T_BYTES + (hf * HC + kk * 16) * 128, L::CHUNK, 1024);
-                        umma_ts(tmem + kBwdTmemAcc, tmem + kBwdTmemDP + hf * HC + kk * 8, bd, idesc_g,
+                        umma_ts(tmem + T::ACC, tmem + T::DS + hf * T::HALF + kk * 8, bd, idesc_g,
                                 (t > 0 || hf > 0 || kk > 0) ? 1u : 0u);
                     }
-                umma_commit(bar(L::B_AE + s));
+                umma_commit(bar(L::B_AE + s));             // K's stage, and dS's columns, are free
             }
-            if (t + 1 < n) {
-                ok = mbar_wait_warp(bar(L::B_BF + s1), ph1, ctl);
-                if (ok) ok = mbar_wait_warp(bar(L::B_AE + s), ph, ctl);   // dS's columns are free
-                if (!ok) break;
-                tc_fence_after();
-                if (elect_one()) {
-                    scores(kBwdTmemDP, TDO, L::OFF_B, s1);
-                    umma_commit(bar(L::B_DPF));
-                    umma_commit(bar(L::B_BE + s1));
-                }
-            }
+            if (!T::SEP && more && !(ok = next_dp(t))) break;
         }
         if (ok && elect_one()) umma_commit(bar(L::B_END));
     } else if (warp >= 2) {
@@ -671,7 +713,7 @@ bwd_q_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
         const int r = static_cast<int>(q4 * 32 + lane);    // query of the block == TMEM lane
         const uint32_t lane_base = (q4 * 32) << 16;
         const float sc = g.scale_log2;
-        const uint32_t ts = tmem + lane_base + kBwdTmemS + hf * HC, td = tmem + lane_base + kBwdTmemDP + hf * HC;
+        const uint32_t ts = tmem + lane_base + T::S + hf * HC, td = tmem + lane_base + T::DP + hf * HC;
         const int qrow = i * BLK + r;
         const bool row_ok = r < BLK && qrow < Nq;
         const size_t st_at = static_cast<size_t>(h) * g.nq * BLK + qrow;
@@ -705,6 +747,10 @@ bwd_q_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
             {
                 float y[HC];
                 tmem_row<HC>(td, y);
+                if constexpr (T::SEP) {
+                    tc_fence_before();
+                    mbar_arrive(bar(L::B_DPE));            // dP may be overwritten by the next one
+                }
 #pragma unroll
                 for (int c = 0; c < HC; c += 2) {
                     fadd2(y[c], y[c + 1], y[c], y[c + 1], nd, nd);
@@ -712,7 +758,9 @@ bwd_q_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
                     pk[c / 2] = pack_bf16x2(y[c], y[c + 1]);
                 }
             }
-            tmem_put<HC>(td, pk);
+            // the previous dS has been read by its product
+            if (T::SEP && t > 0 && !(ok = mbar_wait_warp(bar(L::B_AE + (t - 1) % ST), ((t - 1) / ST) & 1, ctl))) break;
+            tmem_put<HC>(tmem + lane_base + T::DS + hf * T::HALF, pk);
             tmem_wait_st();
             tc_fence_before();
             mbar_arrive(bar(L::B_DSF));
@@ -725,7 +773,7 @@ bwd_q_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
             const size_t at = (static_cast<size_t>(h) * g.N + tok) * D;
 #pragma unroll
             for (int c = hf * (D / 2); c < (hf + 1) * (D / 2); c += 32) {
-                put_grad32(p.dq, at + c, p.grad_f32, tmem + lane_base + kBwdTmemAcc + c, p.scale, n > 0, row_ok);
+                put_grad32(p.dq, at + c, p.grad_f32, tmem + lane_base + T::ACC + c, p.scale, n > 0, row_ok);
                 // the tokens that only take an anchor's output are no queries of a repeat head
                 for (int y = 1; y < copies; ++y)
                     put_grad32(p.dq, at + static_cast<size_t>(y) * g.Wl * D + c, p.grad_f32, 0u, 0.f, false, true);
@@ -753,6 +801,16 @@ bwd_q_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
         tc_fence_after();
         tmem_dealloc(tmem, kTmemCols);
     }
+}
+
+// Both gradients in one launch: the key blocks' items first (four products a tile), then the query blocks'
+// (three), which fill the SMs that run out of the former.
+template <int D, int BLK, int ST>
+__global__ void __launch_bounds__(kBwdThreads, 1) bwd_kernel(const __grid_constant__ BwdMaps m, const __grid_constant__ BwdParams p) {
+    const int n_kv = p.geo.H * p.geo.nk;
+    const int id = static_cast<int>(blockIdx.x);
+    if (id < n_kv) bwd_kv<D, BLK, ST>(m, p, id);
+    else bwd_q<D, BLK, ST>(m, p, id - n_kv);
 }
 
 }  // namespace calib

@@ -8,6 +8,7 @@ library or a non-CUDA tensor raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 from dataclasses import dataclass
@@ -100,14 +101,18 @@ def _check(fn: str, s: int):
 
 
 def _stream():
-    return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
 def _ptr(t: Optional[torch.Tensor]):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _need(t: torch.Tensor, name: str, dtype: torch.dtype, shape=None):
+    # a small call's time is mostly its checks: the usual case is decided by one expression
+    if (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype and t.is_contiguous()
+            and (shape is None or t.shape == shape)):
+        return
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.dtype != dtype:
@@ -118,12 +123,17 @@ def _need(t: torch.Tensor, name: str, dtype: torch.dtype, shape=None):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
-def _on_current_device(**tensors):
+def _on_current_device(*tensors):
     """The calls launch on the current device's stream, so their tensors have to live there."""
-    dev = torch.cuda.current_device()
-    for name, t in tensors.items():
-        if t is not None and t.device.index != dev:
-            raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
+    dev = torch._C._cuda_getDevice()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"a tensor of this call is on {t.device}, the current device is cuda:{dev}")
+
+
+@functools.lru_cache(maxsize=256)
+def _workspace_bytes(fn: str, *sizes) -> int:
+    return getattr(lib(), fn)(*sizes)
 
 
 def device_check():
@@ -273,7 +283,7 @@ def transpose_csr(row_ptr: torch.Tensor, col_idx: torch.Tensor, H: int, nq: int,
     block) the ascending query blocks that keep it, with col_idx's capacity."""
     _need(row_ptr, "row_ptr", torch.int32, (H * nq + 1,))
     _need(col_idx, "col_idx", torch.int16)
-    _on_current_device(row_ptr=row_ptr, col_idx=col_idx)
+    _on_current_device(row_ptr, col_idx)
     t_ptr = torch.empty(H * nk + 1, dtype=torch.int32, device=row_ptr.device)
     t_col = torch.empty_like(col_idx)
     # an empty list still needs valid pointers
@@ -494,12 +504,12 @@ def _bwd(name, q, k, v, out, dout, lse, blist, blist_t, scale, grads, grad_dtype
     dq, dk, dv = (torch.empty((H, N, D), dtype=grad_dtype, device=q.device) if t is None else t for t in grads)
     for t, n in ((dq, "dq"), (dk, "dk"), (dv, "dv")):
         _need(t, n, grad_dtype, (H, N, D))
-    _on_current_device(q=q, k=k, v=v, out=out, dout=dout, lse=lse, dq=dq, dk=dk, dv=dv, row_ptr=blist.row_ptr)
     if blist_t is None:
         blist_t = blist.transpose()
+    _on_current_device(q, k, v, out, dout, lse, dq, dk, dv, blist.row_ptr, blist_t.row_ptr)
     flags = (CALIB_ATTN_OUT_F32 if out.dtype == torch.float32 else 0) | \
         (CALIB_ATTN_GRAD_F32 if grad_dtype == torch.float32 else 0)
-    need = lib().sparse_attn_bwd_workspace(H, N, D, blist.block, n_anchor, flags)
+    need = _workspace_bytes("sparse_attn_bwd_workspace", H, N, D, blist.block, n_anchor, flags)
     space = torch.empty(max(1, need), dtype=torch.uint8, device=q.device)
     cs, ct = blist.c_struct(), blist_t.c_struct()
     sizes = (H, N, D) if geometry is None else (H, D, *geometry)
@@ -622,8 +632,7 @@ def cache_write(cache: KVCache, k_new: torch.Tensor, v_new: torch.Tensor, block_
     _need(k_new, "k_new", torch.bfloat16, (S, Hkv, M, D))
     _need(v_new, "v_new", torch.bfloat16, (S, Hkv, M, D))
     nb = _sequences(block_table, lengths, new_lens, S)
-    _on_current_device(k_new=k_new, v_new=v_new, cache=cache.k, cache_v=cache.v, k_scale=cache.k_scale,
-                       v_scale=cache.v_scale, block_table=block_table, lengths=lengths, new_lens=new_lens)
+    _on_current_device(k_new, v_new, cache.k, cache.v, cache.k_scale, cache.v_scale, block_table, lengths, new_lens)
     _check("calib_cache_write", lib().calib_cache_write(
         _ptr(k_new), _ptr(v_new), _ptr(cache.k), _ptr(cache.v), _ptr(cache.k_scale), _ptr(cache.v_scale),
         _ptr(block_table), _ptr(lengths), _ptr(new_lens), S, Hkv, M, D, block, nb, pages, _stream()))
@@ -654,9 +663,9 @@ def sparse_attn_cached(q: torch.Tensor, cache: KVCache, block_table: torch.Tenso
         lse = torch.empty((S, Hq, M), dtype=torch.float32, device=q.device)
     if lse is not None:
         _need(lse, "lse", torch.float32, (S, Hq, M))
-    _on_current_device(q=q, cache=cache.k, cache_v=cache.v, k_scale=cache.k_scale, v_scale=cache.v_scale,
-                       block_table=block_table, lengths=lengths, new_lens=new_lens, out=out, lse=lse)
-    need = lib().sparse_attn_cached_workspace(S, Hq, Hkv, M, D, block, nb)
+    _on_current_device(q, cache.k, cache.v, cache.k_scale, cache.v_scale, block_table, lengths, new_lens, out, lse,
+                       None if blist is None else blist.row_ptr)
+    need = _workspace_bytes("sparse_attn_cached_workspace", S, Hq, Hkv, M, D, block, nb)
     space = torch.empty(need, dtype=torch.uint8, device=q.device) if need > 0 else None
     cs = None if blist is None else blist.c_struct()
     flags = (CALIB_ATTN_OUT_F32 if out.dtype == torch.float32 else 0) | (CALIB_ATTN_CAUSAL if causal else 0)
