@@ -400,20 +400,37 @@ calib_status bwd_common(const void* q, const void* k, const void* v, const void*
 // ---- 8-bit cache -------------------------------------------------------------------
 constexpr int kSms = 148;
 
-// Query rows per CTA (8 or 16), CTAs over the rows, and parts that a sequence's keys are split into:
-// enough CTAs to give every SM about two, and no part below 512 keys (two steps for each of a CTA's
-// eight warps).
+// How a call's work is shared (see cached_attn_kernel): rows per unit (8 or 16), units per K/V head, and `flat`:
+// shares per K/V head and row tile, or 0 for a CTA per unit.  Own CTAs, and no second launch, where no sequence can
+// be longer than 2048 keys (5 to 8 steps for each of a CTA's warps, about what the cut's merge costs) or the units
+// fill the GPU 8 times and more.  The shares fill the GPU's places once, or twice where once would leave more
+// than a tenth of them empty.
 struct CachedPlan {
-    int nt, tiles, splits;
+    int nt, tiles, flat;
+    long long units, grid;
+    int64_t part_o, part_ml, bytes;   // workspace: offsets of the parts and their statistics; `pieces` is at 0
 };
-CachedPlan cached_plan(int S, int Hq, int Hkv, int M, int B, int nb) {
-    CachedPlan c;
+CachedPlan cached_plan(int S, int Hq, int Hkv, int M, int D, int B, int nb) {
+    CachedPlan c{};
     const long long rows = static_cast<long long>(Hq / Hkv) * M;
     c.nt = rows <= 8 ? 1 : 2;
     c.tiles = cdiv(rows, 8 * c.nt);
-    const long long base = static_cast<long long>(S) * Hkv * c.tiles;
-    const long long most = std::max<long long>(1, static_cast<long long>(nb) * B / 512);
-    c.splits = static_cast<int>(std::min(most, std::max<long long>(1, (2 * kSms + base - 1) / base)));
+    const long long columns = static_cast<long long>(Hkv) * c.tiles;
+    c.units = S * columns;
+    c.grid = c.units;
+    const long long places = kSms * (D == 128 ? 1 : 2);
+    const long long keys = static_cast<long long>(nb) * B;
+    if (keys > 2048 && c.units < 8 * places) {
+        long long shares = std::max(1ll, places / columns);
+        if (shares * columns * 10 < places * 9) shares = std::max(1ll, 2 * places / columns);
+        const long long total = S * (keys / calib::kChunk + calib::kUnitCost);
+        c.flat = static_cast<int>(std::min(shares, std::max(1ll, total / calib::kMinShare)));
+        c.grid = c.flat * columns;
+        const int64_t slots = 2 * c.grid * 8 * c.nt;
+        c.part_o = (c.units * 8 + 15) / 16 * 16;
+        c.part_ml = c.part_o + slots * D * 4;
+        c.bytes = c.part_ml + slots * 8;
+    }
     return c;
 }
 
@@ -448,24 +465,23 @@ bool make_cache_tmap(CUtensorMap* map, const void* base, int D, long long rows) 
 }
 
 template <int D, int B, int NT>
-calib_status launch_cached(const CUtensorMap& tk, const CUtensorMap& tv, const calib::CachedParams& p, int grid,
-                           cudaStream_t st) {
-    using L = calib::CachedSmem<D>;
-    static_assert(L::BYTES <= 232448, "shared memory budget");
+calib_status launch_cached(const CUtensorMap& tk, const CUtensorMap& tv, const calib::CachedParams& p,
+                           const CachedPlan& c, cudaStream_t st) {
+    using L = calib::CachedSmem<D, NT>;
+    static_assert(L::BYTES <= 232448 / L::CTAS - (L::CTAS > 1 ? 1024 : 0), "shared memory budget");
     auto* fn = calib::cached_attn_kernel<D, B, NT>;
     if (calib_status s = ensure_smem(reinterpret_cast<const void*>(fn), L::BYTES)) return s;
-    fn<<<grid, calib::kCachedThreads, L::BYTES, st>>>(tk, tv, p);
+    fn<<<static_cast<int>(c.grid), L::THREADS, L::BYTES, st>>>(tk, tv, p);
     if (calib_status s = launch_status()) return s;
-    if (p.splits == 1) return CALIB_OK;
-    const long long rows = static_cast<long long>(p.S) * p.Hq * p.M;
-    calib::cached_combine_kernel<D><<<static_cast<int>((rows + 3) / 4), 128, 0, st>>>(p, rows);
+    if (!p.flat) return CALIB_OK;
+    calib::cached_combine_kernel<D, NT><<<static_cast<int>(c.units) * NT, 256, 0, st>>>(p);
     return launch_status();
 }
 
 template <int D, int B>
-calib_status launch_cached_nt(int nt, const CUtensorMap& tk, const CUtensorMap& tv, const calib::CachedParams& p,
-                              int grid, cudaStream_t st) {
-    return nt == 1 ? launch_cached<D, B, 1>(tk, tv, p, grid, st) : launch_cached<D, B, 2>(tk, tv, p, grid, st);
+calib_status launch_cached_nt(const CUtensorMap& tk, const CUtensorMap& tv, const calib::CachedParams& p,
+                              const CachedPlan& c, cudaStream_t st) {
+    return c.nt == 1 ? launch_cached<D, B, 1>(tk, tv, p, c, st) : launch_cached<D, B, 2>(tk, tv, p, c, st);
 }
 
 template <int D, int B>
@@ -657,11 +673,16 @@ calib_status calib_transpose_csr(const int32_t* row_ptr, const int16_t* col_idx,
     if (H < 1 || nq < 1 || nk < 1 || nq > 32767 || nk > 32767) return CALIB_ERR_INVALID;
     if (static_cast<long long>(H) * std::max(nq, nk) > (1ll << 31) - 2) return CALIB_ERR_INVALID;
     if (calib_status s = check_device()) return s;
-    const int bytes = calib::kTransCols * cdiv(nq, 32) * 4;
-    if (bytes > 48 * 1024)
-        if (calib_status s = ensure_smem(reinterpret_cast<const void*>(calib::transpose_csr_kernel), 32 * 1024 * 4)) return s;
-    calib::transpose_csr_kernel<<<H * cdiv(nk, calib::kTransCols), calib::kTransThreads, bytes, as_stream(stream)>>>(
-        row_ptr, col_idx, H, nq, nk, t_row_ptr_out, t_col_idx_out);
+    // 128 key blocks per CTA while their bits leave room for two CTAs on an SM (up to about 3000 query blocks),
+    // 32 beyond (131 KB at the most query blocks)
+    const int stride = cdiv(nq, 32) | 1;
+    const int cols = calib::kTransMaxCols * stride * 4 <= 48 * 1024 ? calib::kTransMaxCols : 32;
+    const int bytes = cols * stride * 4 + calib::kTransWarps * 1024 * 2;
+    if (calib_status s = ensure_smem(reinterpret_cast<const void*>(calib::transpose_csr_kernel),
+                                     32 * 1025 * 4 + calib::kTransWarps * 1024 * 2))
+        return s;
+    calib::transpose_csr_kernel<<<H * cdiv(nk, cols), calib::kTransThreads, bytes, as_stream(stream)>>>(
+        row_ptr, col_idx, H, nq, nk, cols, t_row_ptr_out, t_col_idx_out);
     return launch_status();
 }
 
@@ -696,8 +717,7 @@ int64_t sparse_attn_cached_workspace(int S, int Hq, int Hkv, int M, int D, int b
         (D != 64 && D != 128) || static_cast<long long>(S) * Hq > (1ll << 31) - 1 ||
         static_cast<long long>(S) * Hq * M > (1ll << 31) - 1)
         return -1;
-    const CachedPlan c = cached_plan(S, Hq, Hkv, M, block, max_blocks);
-    return c.splits == 1 ? 0 : static_cast<int64_t>(S) * Hq * M * c.splits * (D * 4 + 8);
+    return cached_plan(S, Hq, Hkv, M, D, block, max_blocks).bytes;
 }
 
 calib_status sparse_attn_cached(const void* q, const void* k_cache, const void* v_cache, const float* k_scale,
@@ -720,9 +740,8 @@ calib_status sparse_attn_cached(const void* q, const void* k_cache, const void* 
     const int64_t need = sparse_attn_cached_workspace(S, Hq, Hkv, M, D, block, max_blocks);
     if (need < 0) return CALIB_ERR_UNSUPPORTED;
     if (need > 0 && (!workspace || !aligned16(workspace) || workspace_bytes < need)) return CALIB_ERR_INVALID;
-    const CachedPlan c = cached_plan(S, Hq, Hkv, M, block, max_blocks);
-    const long long grid = static_cast<long long>(S) * Hkv * c.tiles * c.splits;
-    if (grid > (1ll << 31) - 1) return CALIB_ERR_UNSUPPORTED;
+    const CachedPlan c = cached_plan(S, Hq, Hkv, M, D, block, max_blocks);
+    if (c.grid > (1ll << 31) - 1) return CALIB_ERR_UNSUPPORTED;
     calib::CachedParams p{};
     p.q = static_cast<const __nv_bfloat16*>(q);
     p.k_scale = k_scale; p.v_scale = v_scale;
@@ -733,10 +752,14 @@ calib_status sparse_attn_cached(const void* q, const void* k_cache, const void* 
     }
     p.o = o;
     p.lse = lse_opt;
-    p.part_o = static_cast<float*>(workspace);
-    p.part_ml = reinterpret_cast<float2*>(p.part_o + static_cast<size_t>(S) * Hq * M * c.splits * D);
+    if (c.flat) {
+        char* base = static_cast<char*>(workspace);
+        p.pieces = reinterpret_cast<int2*>(base);
+        p.part_o = reinterpret_cast<float*>(base + c.part_o);
+        p.part_ml = reinterpret_cast<float2*>(base + c.part_ml);
+    }
     p.S = S; p.Hq = Hq; p.Hkv = Hkv; p.G = Hq / Hkv; p.M = M; p.nb = max_blocks; p.pages = static_cast<int>(pages);
-    p.tiles = c.tiles; p.splits = c.splits;
+    p.tiles = c.tiles; p.flat = c.flat;
     p.causal = (flags & CALIB_ATTN_CAUSAL) ? 1 : 0;
     p.out_f32 = (flags & CALIB_ATTN_OUT_F32) ? 1 : 0;
     p.scale_log2 = scale * 1.4426950408889634f;
@@ -745,11 +768,8 @@ calib_status sparse_attn_cached(const void* q, const void* k_cache, const void* 
     const long long rows = static_cast<long long>(pages) * Hkv * block;
     if (!make_cache_tmap(&tk, k_cache, D, rows) || !make_cache_tmap(&tv, v_cache, D, rows)) return CALIB_ERR_CUDA;
     cudaStream_t st = as_stream(stream);
-    const int g = static_cast<int>(grid);
-    if (D == 128) return block == 128 ? launch_cached_nt<128, 128>(c.nt, tk, tv, p, g, st)
-                                      : launch_cached_nt<128, 64>(c.nt, tk, tv, p, g, st);
-    return block == 128 ? launch_cached_nt<64, 128>(c.nt, tk, tv, p, g, st)
-                        : launch_cached_nt<64, 64>(c.nt, tk, tv, p, g, st);
+    if (D == 128) return block == 128 ? launch_cached_nt<128, 128>(tk, tv, p, c, st) : launch_cached_nt<128, 64>(tk, tv, p, c, st);
+    return block == 128 ? launch_cached_nt<64, 128>(tk, tv, p, c, st) : launch_cached_nt<64, 64>(tk, tv, p, c, st);
 }
 
 int64_t sparse_attn_bwd_workspace(int H, int N, int D, int block, int n_anchor, uint32_t flags) {

@@ -163,28 +163,38 @@ struct CachedParams {
     const int16_t* col_idx;
     void* o;                              // [S, Hq, M, D] bf16 or fp32
     float* lse;                           // [S, Hq, M] or nullptr
-    float* part_o;                        // workspace [rows][splits][D]
-    float2* part_ml;                      // workspace [rows][splits]
-    int S, Hq, Hkv, G, M, nb, pages, tiles, splits, causal, out_f32;
+    float* part_o;                        // workspace [2 grid][RW][D] (flat)
+    float2* part_ml;                      // workspace [2 grid][RW]
+    int2* pieces;                         // workspace [units]: first slot, count (0: written already)
+    int S, Hq, Hkv, G, M, nb, pages, tiles, causal, out_f32;
+    int flat;                             // shares per K/V head and row tile, or 0: a CTA per unit
     float scale_log2;
     uint64_t timeout_ns;
 };
 
-constexpr int kCachedWarps = 8;
-constexpr int kCachedThreads = 32 * kCachedWarps;
 constexpr int kChunk = 32;                // keys per warp and step
+constexpr int kUnitCost = 16;             // a unit's own cost (Q, merge, output) in chunks
+constexpr int kMinShare = 64;             // no CTA gets less than this (a unit's own cost included)
 constexpr float kPShift = 15.f;           // P is held as 2^(x - m + 15) <= 2^15
 
-template <int D>
+// Warps per CTA and CTAs per SM: a chunk is a chain of shared memory reads, conversions, two products and a
+// softmax, and with two warps a scheduler their latencies, not the memory, set the pace (8 warps per SM at
+// D = 128: 5.4 TB/s, 12: see below); more rows (NT = 2) leave registers for 8 (16 at D = 64).
+template <int D, int NT>
 struct CachedSmem {
-    static constexpr int STAGES = 3;
+    static constexpr int RW = 8 * NT;                                  // query rows
+    static constexpr int WARPS = D == 128 && NT == 1 ? 12 : 8;
+    static constexpr int THREADS = 32 * WARPS;
+    static constexpr int STAGES = 2;
+    static constexpr int CTAS = D == 128 ? 1 : 2;                      // per SM
+    static constexpr int PASSES = D == 128 && NT == 1 ? 2 : 1;         // the warps' results meet in PASSES parts of D
+    static constexpr int DP = D / PASSES;
     static constexpr uint32_t TILE = kChunk * D;                       // one K or V chunk, bytes
-    static constexpr uint32_t RING = kCachedWarps * STAGES * 2 * TILE;
-    static constexpr uint32_t OFF_BAR = RING;
-    static constexpr uint32_t OFF_ML = OFF_BAR + kCachedWarps * STAGES * 8;   // float2 [warps][16]
-    static constexpr uint32_t OFF_MISC = OFF_ML + kCachedWarps * 16 * 8;
+    static constexpr uint32_t OFF_O = WARPS * STAGES * 2 * TILE;       // float [warps][RW][DP]
+    static constexpr uint32_t OFF_ML = OFF_O + WARPS * RW * DP * 4;    // float2 [warps][RW]
+    static constexpr uint32_t OFF_BAR = OFF_ML + WARPS * RW * 8;
+    static constexpr uint32_t OFF_MISC = OFF_BAR + WARPS * STAGES * 8;
     static constexpr uint32_t BYTES = OFF_MISC + 16 + 1024;
-    static_assert(RING >= kCachedWarps * 16 * D * 4, "the warps' results are merged in the ring");
 };
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -213,6 +223,20 @@ __device__ __forceinline__ uint2 lds64(uint32_t a) {
     asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
     return v;
 }
+// Byte b of x and byte b of y, both e4m3, as a half-precision pair 2^-8 times as large, exactly: the byte's
+// sign, exponent and mantissa fields are half precision's top ones with the exponent's first bit left out,
+// so 7 places up and that bit (filled by the sign) cleared is the number over 2^8, subnormal ones too.
+// Three integer instructions where the conversion instruction is one on the slower XU pipe.  NaN comes
+// out as 480 / 2^8.
+template <int b>
+__device__ __forceinline__ uint32_t e4m3_pair_shifted(uint32_t x, uint32_t y) {
+    constexpr uint32_t sel = b | (8 + b) << 4 | (4 + b) << 8 | (12 + b) << 12;   // byte, its sign eight times; twice
+    uint32_t r;
+    asm("prmt.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(x), "r"(y), "n"(sel));
+    return (r << 7) & 0xBF80BF80u;
+}
+// Bytes 0 and 1 have their top bit set where those e4m3 bytes of w are NaN (0x7F or 0xFF).
+__device__ __forceinline__ uint32_t e4m3_nan_bits(uint32_t w) { return (w & 0x7F7Fu) + 0x0101u; }
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y) {
     asm volatile(
         "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::
@@ -223,27 +247,72 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map
 // Weight of a part with maximum m_part in a row with maximum m.  Parts without keys have m_part =
 // -inf and l = 0; a NaN logit leaves l NaN, and it stays NaN here.
 __device__ __forceinline__ float merge_weight(float m_part, float m) { return m == -INFINITY ? 1.f : ex2_approx(m_part - m); }
+// What a row's sum of weighted values, each over 2^8, is multiplied by; 0 without keys.
+__device__ __forceinline__ float out_factor(float l) { return l == 0.f ? 0.f : 256.f / l; }
 // Natural-log LSE of a row from its maximum and its sum of 2^(x - m + kPShift); -inf without keys.
 __device__ __forceinline__ float row_lse(float m, float l) {
     return l == 0.f ? -INFINITY : (m - kPShift + log2f(l)) * 0.69314718055994530942f;
 }
 
+// One cell: sequence s, K/V head h.  Its length and new tokens (0 where they are out of range), and the number
+// of 32-key chunks of the blocks that its query heads attend to.
+struct CachedCell {
+    int s, h, len, n_new, list0, chunks;
+};
+template <int B>
+__device__ __forceinline__ CachedCell cached_cell(const CachedParams& p, int s, int h) {
+    CachedCell c;
+    c.s = s;
+    c.h = h;
+    c.len = p.lengths[c.s];
+    c.n_new = p.new_lens ? p.new_lens[c.s] : p.M;
+    c.list0 = 0;
+    if (c.len < 0 || c.len > static_cast<long long>(p.nb) * B || c.n_new < 0 || c.n_new > p.M || c.n_new > c.len) {
+        raise_status(STATUS_BAD_CACHE);
+        c.len = c.n_new = 0;
+    }
+    int blocks = (c.len + B - 1) / B;
+    if (p.row_ptr && blocks > 0) {
+        const int r = c.h * p.S + c.s;
+        c.list0 = p.row_ptr[r];
+        blocks = p.row_ptr[r + 1] - c.list0;
+        if (c.list0 < 0 || blocks < 0 || blocks > p.nb) {
+            raise_status(STATUS_BAD_LIST);
+            blocks = 0;
+        }
+    }
+    c.chunks = blocks * (B / kChunk);
+    return c;
+}
+
 // Attention of a few query rows over a sequence's cached keys: the G query heads of a K/V head
-// times M query tokens are the rows, 8 * NT of them per CTA.
+// times M query tokens are the rows, 8 * NT of them per unit (a cell and a tile of its rows).
 //
 // What bounds it is reading the cache once: 2 D bytes per key and K/V head.  So a CTA's 8 warps
-// each stream their own 32-key chunks through a 3-deep ring of TMA tiles (24 chunks, up to 192 KB
-// in flight or in use per SM) and meet only at the end.  Rows are few, so they are the N of the
-// products and the keys their M: S^T = K Q^T and O^T = V^T P^T as 16x8x16 MMAs, which wastes
-// nothing at 8 rows where rows as M would fill half of a tile.  (A tcgen05 tile has 128 rows in
-// M; with keys there it would need the 8-bit operands rewritten as 16-bit ones in shared memory
-// first.)
-//   - e4m3 is exact in half precision.  Q is scaled by a power of two per row so that its largest
+// each stream their own 32-key chunks through a ring of TMA tiles (up to 192 KB in flight or in use
+// per SM) and meet only at a unit's end, whose loads for the next unit are already under way.
+//
+// Work is shared in two ways.  `flat`: per K/V head (and row tile), all sequences' chunks are one line, cut
+// into `flat` equal shares, one per CTA and one CTA per place on the GPU; each unit counts for 16 chunks
+// more, about what its Q load, merge and output take, so that many short sequences spread as well as few long
+// ones.  A unit that a cut divides leaves its parts in the workspace for cached_combine_kernel.  The heads' cuts
+// fall on the same places, and CTAs with the same share are neighbours, so the heads of a page, which lie side by
+// side in memory, are read at the same time (4 x 131072 tokens, 8 heads: 216 us with one line through all heads
+// on 148 SMs, 190 us with the heads side by side on 128).  Otherwise one CTA per unit and no second launch: where a
+// sequence is short, or the units fill the GPU several times anyway.
+//
+// Rows are few, so they are the N of the products and the keys their M: S^T = K Q^T and
+// O^T = V^T P^T as 16x8x16 MMAs, which wastes nothing at 8 rows where rows as M would fill half of a
+// tile.  (A tcgen05 tile has 128 rows in M; with keys there it would need the 8-bit operands
+// rewritten as 16-bit ones in shared memory first.)
+//   - e4m3 is exact in half precision: K and half of V by the conversion instruction, the
+//     other half of V by integer ones (all of them on the XU pipe, 16 lanes a clock, kept that busy to
+//     100%); the NaNs of that half are looked for apart, and make their chunk's product NaN.  Q is scaled by a power of two per row so that its largest
 //     value is in [2^14, 2^15): bf16's 8 bits fit half's 11, and values down to 2^-30 of the
 //     largest stay exact.  P is kept as 2^(x - m + 15), so that half precision holds weights down
-//     to 2^-39 of the largest; its rounding (2^-12 relative) is to nearest and has no bias.
+//     to 2^-39 of the largest; its rounding (2^-11 relative at most) is to nearest, without bias.
 //   - A tile row of K is read in an order of d that gives a thread 16 contiguous bytes, the same
-//     order for Q; a column of V^T likewise, so a thread ends up with 16 contiguous values of O.
+//     order for Q; a column of V^T likewise, so a thread ends up with D / 8 contiguous values of O.
 //   - P^T leaves the first product as rows of keys and enters the second as columns: two 8x8
 //     transposes in registers.
 //   - Each chunk's product goes to its own accumulator, and O = O 2^(m_old - m) + scale_v O_chunk
@@ -251,50 +320,22 @@ __device__ __forceinline__ float row_lse(float m, float l) {
 // Shared memory tiles are swizzled by TMA; keys are assigned to MMA rows (a odd: a ^ 4) so that
 // both K's and V's reads touch each bank once.
 template <int D, int B, int NT>
-__global__ void __launch_bounds__(kCachedThreads) cached_attn_kernel(const __grid_constant__ CUtensorMap tm_k,
-                                                                     const __grid_constant__ CUtensorMap tm_v,
-                                                                     const CachedParams p) {
-    using L = CachedSmem<D>;
-    constexpr int ST = L::STAGES, KS = D / 16, MT = D / 16, RW = 8 * NT;
-    constexpr int CPB = B / kChunk;
+__global__ void __launch_bounds__((CachedSmem<D, NT>::THREADS), (CachedSmem<D, NT>::CTAS))
+cached_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                   const __grid_constant__ CachedParams p) {
+    using L = CachedSmem<D, NT>;
+    constexpr int ST = L::STAGES, KS = D / 16, MT = D / 16, RW = L::RW, CPB = B / kChunk, W = L::WARPS;
     extern __shared__ uint8_t smem_raw[];
+    __shared__ long long scan_sum[W];
+    __shared__ int start[2];                                // the share's first sequence, and its position there
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::OFF_MISC);
+    float* so = reinterpret_cast<float*>(smem + L::OFF_O);
+    float2* sml = reinterpret_cast<float2*>(smem + L::OFF_ML);
     const int warp = static_cast<int>(warp_id()), lane = static_cast<int>(lane_id());
     const int a8 = lane >> 2, t4 = lane & 3;
     const uint32_t ring = smem_u32(smem) + warp * ST * 2 * L::TILE;
     const uint32_t bars = smem_u32(smem + L::OFF_BAR) + warp * ST * 8;
-
-    // ---- the CTA's rows and keys ------------------------------------------------
-    int x = blockIdx.x;
-    const int split = x % p.splits;
-    x /= p.splits;
-    const int tile = x % p.tiles;
-    x /= p.tiles;
-    const int h = x % p.Hkv, s = x / p.Hkv;
-    const int rows = p.G * p.M;
-    const int row0 = tile * RW;
-    int len = p.lengths[s];
-    int n_new = p.new_lens ? p.new_lens[s] : p.M;
-    if (len < 0 || len > static_cast<long long>(p.nb) * B || n_new < 0 || n_new > p.M || n_new > len) {
-        if (threadIdx.x == 0) raise_status(STATUS_BAD_CACHE);
-        len = n_new = 0;
-    }
-    int nblk = (len + B - 1) / B, list0 = 0;
-    if (p.row_ptr) {
-        const int r = h * p.S + s;
-        list0 = p.row_ptr[r];
-        const int n = p.row_ptr[r + 1] - list0;
-        if (list0 < 0 || n < 0 || n > p.nb) {
-            if (threadIdx.x == 0) raise_status(STATUS_BAD_LIST);
-            nblk = 0;
-        } else if (nblk > 0) {
-            nblk = n;
-        }
-    }
-    const int n_chunks = nblk * CPB;
-    const int c_beg = static_cast<int>(static_cast<long long>(n_chunks) * split / p.splits);
-    const int c_end = static_cast<int>(static_cast<long long>(n_chunks) * (split + 1) / p.splits);
 
     if (threadIdx.x == 0) *abort_flag = 0;
     if (lane == 0) {
@@ -303,366 +344,513 @@ __global__ void __launch_bounds__(kCachedThreads) cached_attn_kernel(const __gri
         tma_prefetch_desc(&tm_k);
         tma_prefetch_desc(&tm_v);
     }
-    __syncthreads();
     const WaitCtl ctl{abort_flag, p.timeout_ns};
 
-    // chunks c_beg + warp, + 8, ...: 32 of them at a time are looked up, one per lane
-    const int first = c_beg + warp;
-    const int mine = c_end > first ? (c_end - first + kCachedWarps - 1) / kCachedWarps : 0;
+    // ---- the CTA's share --------------------------------------------------------
+    const int columns = p.Hkv * p.tiles;                    // (K/V head, row tile)
+    long long total = 0, left = 0, pos = 0;                 // flat: of the column; of the share; where it stands
+    int shares = 1, share = 0, v0 = 0;                      // v0: position in the unit (chunks, then its own cost)
+    int seq = 0;
+    const int column = static_cast<int>(blockIdx.x) % columns, tile = column % p.tiles, head = column / p.tiles;
+    if (p.flat) {
+        share = static_cast<int>(blockIdx.x) / columns;
+        const int per = (p.S + L::THREADS - 1) / L::THREADS;
+        const int lo = min(p.S, static_cast<int>(threadIdx.x) * per), hi = min(p.S, lo + per);
+        long long mine = 0;
+        for (int x = lo; x < hi; ++x) mine += cached_cell<B>(p, x, head).chunks + kUnitCost;
+        long long incl = mine;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const long long y = __shfl_up_sync(0xffffffffu, incl, off);
+            if (lane >= off) incl += y;
+        }
+        if (lane == 31) scan_sum[warp] = incl;
+        __syncthreads();
+        for (int w = 0; w < W; ++w) {
+            if (w < warp) incl += scan_sum[w];
+            total += scan_sum[w];
+        }
+        shares = static_cast<int>(min(static_cast<long long>(p.flat), max(1ll, total / kMinShare)));
+        if (share >= shares) return;
+        pos = total * share / shares;
+        left = total * (share + 1) / shares - pos;
+        if (pos >= incl - mine && pos < incl) {             // one thread: its sequences hold the first position
+            long long at = incl - mine;
+            for (int x = lo; x < hi; ++x) {
+                const int n = cached_cell<B>(p, x, head).chunks + kUnitCost;
+                if (pos < at + n) {
+                    start[0] = x;
+                    start[1] = static_cast<int>(pos - at);
+                    break;
+                }
+                at += n;
+            }
+        }
+        __syncthreads();
+        seq = start[0];
+        v0 = start[1];
+    } else {
+        seq = static_cast<int>(blockIdx.x) / columns;
+        __syncthreads();
+    }
+
+    // ---- a segment: the part [c0, c1) of a unit's chunks that falls to this CTA -----
+    CachedCell cl = cached_cell<B>(p, seq, head);
+    int c0 = 0, c1 = cl.chunks;
+    bool first_seg = true;
+    auto cut = [&]() {
+        const int take = static_cast<int>(min(left, static_cast<long long>(cl.chunks + kUnitCost - v0)));
+        c0 = min(v0, cl.chunks);
+        c1 = min(v0 + take, cl.chunks);
+        left -= take;
+    };
+    auto next_unit = [&]() -> bool {                        // flat only
+        pos += cl.chunks + kUnitCost - v0;
+        v0 = 0;
+        if (left <= 0) return false;
+        cl = cached_cell<B>(p, ++seq, head);
+        cut();
+        return true;
+    };
+    if (p.flat) {
+        cut();
+        if (v0 > 0 && c0 == c1 && !next_unit()) return;     // the share begins in a unit's own cost: nothing to do there
+    }
+
+    // chunks c0 + warp, + 8, ...: 32 of them at a time are looked up, one per lane
+    int mine = 0;
     int look_y = -1, look_key = 0;
     float look_ks = 0.f, look_vs = 0.f;
     auto look_up = [&](int n0) {                            // steps n0 .. n0 + 31
         const int n = n0 + lane;
         look_y = -1;
         if (n < mine) {
-            const int c = first + n * kCachedWarps;
+            const int c = c0 + warp + n * W;
             int blk = c / CPB;
-            if (p.row_ptr) blk = p.col_idx[list0 + blk];
+            if (p.row_ptr) blk = p.col_idx[cl.list0 + blk];
             look_key = blk * B + c % CPB * kChunk;
-            if (blk >= 0 && look_key < len) {
-                const int page = p.table[static_cast<size_t>(s) * p.nb + blk];
+            if (blk >= 0 && look_key < cl.len) {
+                const int page = p.table[static_cast<size_t>(cl.s) * p.nb + blk];
                 if (page >= 0 && page < p.pages) {
-                    const int cell = page * p.Hkv + h;
-                    look_y = cell * B + c % CPB * kChunk;
-                    look_ks = p.k_scale[cell];
-                    look_vs = p.v_scale[cell];
+                    const int at = page * p.Hkv + cl.h;
+                    look_y = at * B + c % CPB * kChunk;
+                    look_ks = p.k_scale[at];
+                    look_vs = p.v_scale[at];
                 } else {
                     raise_status(STATUS_BAD_CACHE);
                 }
             }
         }
     };
-    // A chunk without keys (past the sequence, or its page unusable) has y = -1: not loaded.
-    auto issue = [&](int n, int y) {
-        if (y >= 0 && lane == 0) {
-            const int st = n % ST;
-            mbar_arrive_expect_tx(bars + 8 * st, 2 * L::TILE);
-            tma_load_2d(ring + st * 2 * L::TILE, &tm_k, bars + 8 * st, 0, y);
-            tma_load_2d(ring + st * 2 * L::TILE + L::TILE, &tm_v, bars + 8 * st, 0, y);
-        }
-    };
-    // each step's place in the cache, first key and scales are passed along as it moves from being
-    // issued to being used
-    int y_q[ST] = {}, key_q[ST] = {};
-    float ks_q[ST] = {}, vs_q[ST] = {};
+    // Each step's place in the cache, first key and scales are passed along from its issue to its use.  A
+    // chunk without keys (past the sequence, or its page unusable) has y = -1 and is not loaded.
+    int y_q[ST - 1] = {}, key_q[ST - 1] = {};
+    float ks_q[ST - 1] = {}, vs_q[ST - 1] = {};
+    int it = 0;                                             // steps of earlier segments: step n uses stage (it + n) % ST
     uint32_t phase = 0;                                     // bit st: parity of stage st's next wait
-
+    uint32_t flying = 0;                                    // bit st: a load that nobody has waited for
     auto fetch = [&](int n, int slot) {                     // look up (from registers) and issue step n
         if ((n & 31) == 0) look_up(n);
         y_q[slot] = __shfl_sync(0xffffffffu, look_y, n & 31);
         key_q[slot] = __shfl_sync(0xffffffffu, look_key, n & 31);
         ks_q[slot] = __shfl_sync(0xffffffffu, look_ks, n & 31);
         vs_q[slot] = __shfl_sync(0xffffffffu, look_vs, n & 31);
-        issue(n, y_q[slot]);
+        if (y_q[slot] >= 0) {
+            const int st = (it + n) % ST;
+            flying |= 1u << st;
+            if (lane == 0) {
+                mbar_arrive_expect_tx(bars + 8 * st, 2 * L::TILE);
+                tma_load_2d(ring + st * 2 * L::TILE, &tm_k, bars + 8 * st, 0, y_q[slot]);
+                tma_load_2d(ring + st * 2 * L::TILE + L::TILE, &tm_v, bars + 8 * st, 0, y_q[slot]);
+            }
+        }
     };
+    auto begin_segment = [&]() {
+        mine = c1 - c0 > warp ? (c1 - c0 - warp + W - 1) / W : 0;
 #pragma unroll
-    for (int n = 0; n < ST - 1; ++n) {
-        if (n < mine) fetch(n, n);
-    }
-
-    // ---- Q: rows a8 + 8 nt, scaled by a power of two, as the B operand -----------
-    uint32_t qf[NT][KS][2];
-    float fac[NT][2];                                       // scale_log2 / that power, for rows 2 t4, 2 t4 + 1
-    int limit[NT][2];                                       // keys those rows may see
-    int lim_min = len;
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-        const int r = row0 + nt * 8 + a8;
-        uint4 w[D / 64][2];
-        float amax = 0.f;
-#pragma unroll
-        for (int c = 0; c < D / 64; ++c) {
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                w[c][e] = make_uint4(0, 0, 0, 0);
-                if (r < rows)
-                    w[c][e] = *reinterpret_cast<const uint4*>(
-                        p.q + ((static_cast<size_t>(s) * p.Hq + static_cast<size_t>(h) * p.G) * p.M + r) * D + c * 64 +
-                        t4 * 16 + e * 8);
-                const uint32_t u[4] = {w[c][e].x, w[c][e].y, w[c][e].z, w[c][e].w};
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(u[i] << 16)), fabsf(__uint_as_float(u[i] & 0xFFFF0000u))));
-            }
-        }
-        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-        // exponent field of the largest: 2^(e - 127) <= amax < 2^(e - 126)
-        const int ef = max(15, min(254, static_cast<int>(__float_as_uint(amax) >> 23)));
-        const float up = __uint_as_float(static_cast<uint32_t>(127 + 14 - (ef - 127)) << 23);   // 2^(14 - (ef - 127))
-        const float down = __uint_as_float(static_cast<uint32_t>(max(1, 127 - 14 + (ef - 127))) << 23);
-#pragma unroll
-        for (int c = 0; c < D / 64; ++c)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const uint32_t u[4] = {w[c][e].x, w[c][e].y, w[c][e].z, w[c][e].w};
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    qf[nt][c * 4 + e * 2 + i / 2][i & 1] =
-                        pack_f16x2(__uint_as_float(u[i] << 16) * up, __uint_as_float(u[i] & 0xFFFF0000u) * up);
-            }
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            fac[nt][e] = __shfl_sync(0xffffffffu, down, (2 * t4 + e) * 4) * p.scale_log2;
-            const int rr = row0 + nt * 8 + 2 * t4 + e;
-            const int m = rr % p.M;
-            limit[nt][e] = rr < rows && m < n_new ? (p.causal ? len - n_new + m + 1 : len) : 0;
-            lim_min = min(lim_min, limit[nt][e]);
-        }
-    }
-    lim_min = __reduce_min_sync(0xffffffffu, lim_min);
-
-    float o[NT][MT][4], m_run[NT][2], l_run[NT][2];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) o[nt][mt][e] = 0.f;
-        m_run[nt][0] = m_run[nt][1] = -INFINITY;
-        l_run[nt][0] = l_run[nt][1] = 0.f;
-    }
+        for (int n = 0; n < ST - 1; ++n)
+            if (n < mine) fetch(n, n);
+    };
+    begin_segment();
 
     const int rho = (a8 & 1) ? a8 ^ 4 : a8;                 // key of MMA row a8 (and + 8)
     const int vk0 = 2 * t4, vk1 = (2 * t4 + 1) ^ 4;         // keys of MMA rows 2 t4, 2 t4 + 1
-    int slot = 0;
+    const int rows = p.G * p.M;
     bool ok = true;
-    for (int n = 0; n < mine; ++n) {
-        const int y = y_q[0], key0 = key_q[0];
-        const float ks = ks_q[0], vs = vs_q[0];
+    while (true) {
+        // ---- Q: rows a8 + 8 nt, scaled by a power of two, as the B operand -------
+        const int row0 = tile * RW;
+        const size_t out_row = (static_cast<size_t>(cl.s) * p.Hq + static_cast<size_t>(cl.h) * p.G) * p.M + row0;
+        uint32_t qf[NT][KS][2];
+        float fac[NT][2];                                   // scale_log2 / that power, for rows 2 t4, 2 t4 + 1
+        int limit[NT][2];                                   // keys those rows may see
+        int lim_min = cl.len;
 #pragma unroll
-        for (int i = 0; i + 1 < ST; ++i) {
-            y_q[i] = y_q[i + 1];
-            key_q[i] = key_q[i + 1];
-            ks_q[i] = ks_q[i + 1];
-            vs_q[i] = vs_q[i + 1];
+        for (int nt = 0; nt < NT; ++nt) {
+            const int r = nt * 8 + a8;
+            uint4 w[D / 64][2];
+            float amax = 0.f;
+#pragma unroll
+            for (int c = 0; c < D / 64; ++c) {
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    w[c][e] = make_uint4(0, 0, 0, 0);
+                    if (row0 + r < rows)
+                        w[c][e] = *reinterpret_cast<const uint4*>(p.q + (out_row + r) * D + c * 64 + t4 * 16 + e * 8);
+                    const uint32_t u[4] = {w[c][e].x, w[c][e].y, w[c][e].z, w[c][e].w};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(u[i] << 16)), fabsf(__uint_as_float(u[i] & 0xFFFF0000u))));
+                }
+            }
+            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+            // exponent field of the largest: 2^(e - 127) <= amax < 2^(e - 126); up = 2^(14 - (e - 127)), down = 1 / up
+            const int ef = max(15, min(254, static_cast<int>(__float_as_uint(amax) >> 23)));
+            const float up = __uint_as_float(static_cast<uint32_t>(268 - ef) << 23);
+            const float down = __uint_as_float(static_cast<uint32_t>(ef - 14) << 23);
+#pragma unroll
+            for (int c = 0; c < D / 64; ++c)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const uint32_t u[4] = {w[c][e].x, w[c][e].y, w[c][e].z, w[c][e].w};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        qf[nt][c * 4 + e * 2 + i / 2][i & 1] =
+                            pack_f16x2(__uint_as_float(u[i] << 16) * up, __uint_as_float(u[i] & 0xFFFF0000u) * up);
+                }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                fac[nt][e] = __shfl_sync(0xffffffffu, down, (2 * t4 + e) * 4) * p.scale_log2;
+                const int rr = row0 + nt * 8 + 2 * t4 + e;
+                const int m = rr % p.M;
+                limit[nt][e] = rr < rows && m < cl.n_new ? (p.causal ? cl.len - cl.n_new + m + 1 : cl.len) : 0;
+                lim_min = min(lim_min, limit[nt][e]);
+            }
         }
-        // the stage read in the previous step is free: every lane has its values in registers
-        __syncwarp();
-        if (n + ST - 1 < mine) fetch(n + ST - 1, ST - 2);
-        const int st = slot;
-        slot = slot + 1 == ST ? 0 : slot + 1;
-        if (y < 0) continue;
-        ok = mbar_wait_warp(bars + 8 * st, (phase >> st) & 1u, ctl);
-        if (!ok) break;
-        phase ^= 1u << st;
-        const uint32_t kt = ring + st * 2 * L::TILE, vt = kt + L::TILE;
+        lim_min = __reduce_min_sync(0xffffffffu, lim_min);
 
-        // S^T = K Q^T, two 16-key tiles
-        float sc[2][NT][4];
+        float o[NT][MT][4], m_run[NT][2], l_run[NT][2];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[nt][mt][e] = 0.f;
+            m_run[nt][0] = m_run[nt][1] = -INFINITY;
+            l_run[nt][0] = l_run[nt][1] = 0.f;
+        }
+
+        for (int n = 0; n < mine; ++n) {
+            const int y = y_q[0], key0 = key_q[0];
+            const float ks = ks_q[0], vs = vs_q[0];
+#pragma unroll
+            for (int i = 0; i + 1 < ST - 1; ++i) {
+                y_q[i] = y_q[i + 1];
+                key_q[i] = key_q[i + 1];
+                ks_q[i] = ks_q[i + 1];
+                vs_q[i] = vs_q[i + 1];
+            }
+            // the stage read in the previous step is free: every lane has its values in registers
+            __syncwarp();
+            if (n + ST - 1 < mine) fetch(n + ST - 1, ST - 2);
+            if (y < 0) continue;
+            const int st = (it + n) % ST;
+            ok = mbar_wait_warp(bars + 8 * st, (phase >> st) & 1u, ctl);
+            if (!ok) break;
+            phase ^= 1u << st;
+            flying &= ~(1u << st);
+            const uint32_t kt = ring + st * 2 * L::TILE, vt = kt + L::TILE;
+
+            // S^T = K Q^T, two 16-key tiles
+            float sc[2][NT][4];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) sc[i][nt][e] = 0.f;
+#pragma unroll
+                for (int c = 0; c < D / 64; ++c) {
+                    const int r0 = i * 16 + rho, r1 = r0 + 8;
+                    uint4 k0, k1;
+                    if constexpr (D == 128) {
+                        k0 = lds128(kt + r0 * 128 + (((c * 4 + t4) ^ (r0 & 7)) << 4));
+                        k1 = lds128(kt + r1 * 128 + (((c * 4 + t4) ^ (r1 & 7)) << 4));
+                    } else {
+                        k0 = lds128(kt + r0 * 64 + ((t4 ^ ((r0 >> 1) & 3)) << 4));
+                        k1 = lds128(kt + r1 * 64 + ((t4 ^ ((r1 >> 1) & 3)) << 4));
+                    }
+                    const uint32_t u0[4] = {k0.x, k0.y, k0.z, k0.w}, u1[4] = {k1.x, k1.y, k1.z, k1.w};
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk) {
+                        const uint32_t a0 = e4m3x2_to_f16x2(u0[kk]), a2 = e4m3x2_hi_to_f16x2(u0[kk]);
+                        const uint32_t a1 = e4m3x2_to_f16x2(u1[kk]), a3 = e4m3x2_hi_to_f16x2(u1[kk]);
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+                            mma_f16(sc[i][nt], a0, a1, a2, a3, qf[nt][c * 4 + kk][0], qf[nt][c * 4 + kk][1]);
+                    }
+                }
+            }
+            // log2-domain logits, masks, running maximum
+            uint32_t pf[2][NT][2];
+            float alpha[NT][2];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                const float f0 = fac[nt][0] * ks, f1 = fac[nt][1] * ks;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    sc[i][nt][0] *= f0;
+                    sc[i][nt][1] *= f1;
+                    sc[i][nt][2] *= f0;
+                    sc[i][nt][3] *= f1;
+                }
+                if (key0 + kChunk > lim_min) {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (key0 + i * 16 + rho + (e >> 1) * 8 >= limit[nt][e & 1]) sc[i][nt][e] = -INFINITY;
+                }
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float mx = fmaxf(fmaxf(sc[0][nt][e], sc[0][nt][e + 2]), fmaxf(sc[1][nt][e], sc[1][nt][e + 2]));
+                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+                    const float m_new = fmaxf(m_run[nt][e], mx);
+                    const float ref = m_new == -INFINITY ? 0.f : m_new - kPShift;
+                    alpha[nt][e] = ex2_approx(m_run[nt][e] - (m_new == -INFINITY ? 0.f : m_new));
+                    m_run[nt][e] = m_new;
+                    float add = 0.f;
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        sc[i][nt][e] = ex2_approx(sc[i][nt][e] - ref);
+                        sc[i][nt][e + 2] = ex2_approx(sc[i][nt][e + 2] - ref);
+                        add += sc[i][nt][e] + sc[i][nt][e + 2];
+                    }
+                    l_run[nt][e] = l_run[nt][e] * alpha[nt][e] + add;
+                }
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    pf[i][nt][0] = transpose_8x8(pack_f16x2(sc[i][nt][0], sc[i][nt][1]));
+                    pf[i][nt][1] = transpose_8x8(pack_f16x2(sc[i][nt][2], sc[i][nt][3]));
+                }
+            }
+            // O^T of this chunk = V^T P^T
+            float oc[NT][MT][4];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) sc[i][nt][e] = 0.f;
+                for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-            for (int c = 0; c < D / 64; ++c) {
-                const int r0 = i * 16 + rho, r1 = r0 + 8;
-                uint4 k0, k1;
-                if constexpr (D == 128) {
-                    k0 = lds128(kt + r0 * 128 + (((c * 4 + t4) ^ (r0 & 7)) << 4));
-                    k1 = lds128(kt + r1 * 128 + (((c * 4 + t4) ^ (r1 & 7)) << 4));
-                } else {
-                    k0 = lds128(kt + r0 * 64 + ((t4 ^ ((r0 >> 1) & 3)) << 4));
-                    k1 = lds128(kt + r1 * 64 + ((t4 ^ ((r1 >> 1) & 3)) << 4));
-                }
-                const uint32_t u0[4] = {k0.x, k0.y, k0.z, k0.w}, u1[4] = {k1.x, k1.y, k1.z, k1.w};
-#pragma unroll
-                for (int kk = 0; kk < 4; ++kk) {
-                    const uint32_t a0 = e4m3x2_to_f16x2(u0[kk]), a2 = e4m3x2_hi_to_f16x2(u0[kk]);
-                    const uint32_t a1 = e4m3x2_to_f16x2(u1[kk]), a3 = e4m3x2_hi_to_f16x2(u1[kk]);
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) mma_f16(sc[i][nt], a0, a1, a2, a3, qf[nt][c * 4 + kk][0], qf[nt][c * 4 + kk][1]);
-                }
-            }
-        }
-        // log2-domain logits, masks, running maximum
-        uint32_t pf[2][NT][2];
-        float alpha[NT][2];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            const float f0 = fac[nt][0] * ks, f1 = fac[nt][1] * ks;
+                    for (int e = 0; e < 4; ++e) oc[nt][mt][e] = 0.f;
+            const bool tail = key0 + kChunk > cl.len;       // bytes behind the sequence can be anything
+            uint32_t nan = 0u;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                sc[i][nt][0] *= f0;
-                sc[i][nt][1] *= f1;
-                sc[i][nt][2] *= f0;
-                sc[i][nt][3] *= f1;
-            }
-            if (key0 + kChunk > lim_min) {
+                uint32_t u[4][D / 32];
 #pragma unroll
-                for (int i = 0; i < 2; ++i)
+                for (int kx = 0; kx < 4; ++kx) {
+                    const int r = i * 16 + (kx & 1 ? vk1 : vk0) + (kx >> 1) * 8;
+                    if constexpr (D == 128) {
+                        const uint4 w = lds128(vt + r * 128 + ((a8 ^ (r & 7)) << 4));
+                        u[kx][0] = w.x; u[kx][1] = w.y; u[kx][2] = w.z; u[kx][3] = w.w;
+                    } else {
+                        const uint2 w = lds64(vt + r * 64 + (((a8 >> 1) ^ ((r >> 1) & 3)) << 4) + (a8 & 1) * 8);
+                        u[kx][0] = w.x; u[kx][1] = w.y;
+                    }
+                    if (tail && key0 + r >= cl.len) {
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if (key0 + i * 16 + rho + (e >> 1) * 8 >= limit[nt][e & 1]) sc[i][nt][e] = -INFINITY;
-            }
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                float mx = fmaxf(fmaxf(sc[0][nt][e], sc[0][nt][e + 2]), fmaxf(sc[1][nt][e], sc[1][nt][e + 2]));
-                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-                const float m_new = fmaxf(m_run[nt][e], mx);
-                const float ref = m_new == -INFINITY ? 0.f : m_new - kPShift;
-                alpha[nt][e] = ex2_approx(m_run[nt][e] - (m_new == -INFINITY ? 0.f : m_new));
-                m_run[nt][e] = m_new;
-                float add = 0.f;
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    sc[i][nt][e] = ex2_approx(sc[i][nt][e] - ref);
-                    sc[i][nt][e + 2] = ex2_approx(sc[i][nt][e + 2] - ref);
-                    add += sc[i][nt][e] + sc[i][nt][e + 2];
+                        for (int e = 0; e < D / 32; ++e) u[kx][e] = 0u;
+                    }
                 }
-                l_run[nt][e] = l_run[nt][e] * alpha[nt][e] + add;
-            }
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                pf[i][nt][0] = transpose_8x8(pack_f16x2(sc[i][nt][0], sc[i][nt][1]));
-                pf[i][nt][1] = transpose_8x8(pack_f16x2(sc[i][nt][2], sc[i][nt][3]));
+                for (int e = 0; e < D / 32; ++e) {
+                    nan |= e4m3_nan_bits(u[0][e]) | e4m3_nan_bits(u[1][e]);
+                    nan |= e4m3_nan_bits(u[2][e]) | e4m3_nan_bits(u[3][e]);
+                    const uint32_t a0 = e4m3_pair_shifted<0>(u[0][e], u[1][e]), a1 = e4m3_pair_shifted<1>(u[0][e], u[1][e]);
+                    const uint32_t a2 = e4m3_pair_shifted<0>(u[2][e], u[3][e]), a3 = e4m3_pair_shifted<1>(u[2][e], u[3][e]);
+                    const uint32_t x0 = __byte_perm(u[0][e], u[1][e], 0x7362), x1 = __byte_perm(u[2][e], u[3][e], 0x7362);
+                    const uint32_t b0 = e4m3x2_to_f16x2(x0), b1 = e4m3x2_hi_to_f16x2(x0);
+                    const uint32_t b2 = e4m3x2_to_f16x2(x1), b3 = e4m3x2_hi_to_f16x2(x1);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        mma_f16(oc[nt][e * 2], a0, a1, a2, a3, pf[i][nt][0], pf[i][nt][1]);
+                        mma_f16(oc[nt][e * 2 + 1], b0, b1, b2, b3, pf[i][nt][0], pf[i][nt][1]);
+                    }
+                }
             }
+            // even tiles hold values over 2^8 (bytes 0 and 1), odd ones the values themselves; O is kept over 2^8
+            const float vs_mt[2] = {__any_sync(0xffffffffu, (nan & 0x8080u) != 0u) ? __int_as_float(0x7FC00000) : vs,
+                                    vs * 0.00390625f};
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) o[nt][mt][e] = o[nt][mt][e] * alpha[nt][e & 1] + oc[nt][mt][e] * vs_mt[mt & 1];
         }
-        // O^T of this chunk = V^T P^T
-        float oc[NT][MT][4];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) oc[nt][mt][e] = 0.f;
-        const bool tail = key0 + kChunk > len;              // bytes behind the sequence can be anything
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            uint32_t u[4][D / 32];
-#pragma unroll
-            for (int kx = 0; kx < 4; ++kx) {
-                const int r = i * 16 + (kx & 1 ? vk1 : vk0) + (kx >> 1) * 8;
-                if constexpr (D == 128) {
-                    const uint4 w = lds128(vt + r * 128 + ((a8 ^ (r & 7)) << 4));
-                    u[kx][0] = w.x; u[kx][1] = w.y; u[kx][2] = w.z; u[kx][3] = w.w;
-                } else {
-                    const uint2 w = lds64(vt + r * 64 + (((a8 >> 1) ^ ((r >> 1) & 3)) << 4) + (a8 & 1) * 8);
-                    u[kx][0] = w.x; u[kx][1] = w.y;
-                }
-                if (tail && key0 + r >= len) {
-#pragma unroll
-                    for (int e = 0; e < D / 32; ++e) u[kx][e] = 0u;
-                }
-            }
-#pragma unroll
-            for (int e = 0; e < D / 32; ++e) {
-#pragma unroll
-                for (int hf = 0; hf < 2; ++hf) {
-                    const uint32_t x0 = __byte_perm(u[0][e], u[1][e], hf ? 0x7362 : 0x5140);
-                    const uint32_t x1 = __byte_perm(u[2][e], u[3][e], hf ? 0x7362 : 0x5140);
-                    const uint32_t a0 = e4m3x2_to_f16x2(x0), a1 = e4m3x2_hi_to_f16x2(x0);
-                    const uint32_t a2 = e4m3x2_to_f16x2(x1), a3 = e4m3x2_hi_to_f16x2(x1);
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) mma_f16(oc[nt][e * 2 + hf], a0, a1, a2, a3, pf[i][nt][0], pf[i][nt][1]);
-                }
-            }
-        }
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) o[nt][mt][e] = o[nt][mt][e] * alpha[nt][e & 1] + oc[nt][mt][e] * vs;
-    }
+        it = (it + mine) % ST;
 
-    // ---- the warps' results meet in shared memory -------------------------------
-    if (!ok && lane == 0) {                                 // copies still in flight end before the ring is reused
+        // ---- where the result goes ----------------------------------------------
+        const bool whole = c0 == 0 && c1 == cl.chunks;
+        const int slot = 2 * static_cast<int>(blockIdx.x) + (first_seg ? 0 : 1);
+        if (p.flat && c0 == 0 && v0 == 0 && threadIdx.x == 0) {
+            // the share that holds the unit's last chunk is the last one that begins at or before it
+            const long long last = pos + cl.chunks - 1;
+            const int g1 = static_cast<int>(((last + 1) * shares + total - 1) / total) - 1;
+            p.pieces[(static_cast<size_t>(cl.s) * p.Hkv + cl.h) * p.tiles + tile] =
+                whole ? make_int2(0, 0) : make_int2(slot, g1 - share + 1);
+        }
+        // ---- the next segment, and its first loads --------------------------------
+        bool more = false;
+        if (p.flat && ok && next_unit()) {
+            more = true;
+            __syncwarp();
+            begin_segment();
+        }
+        // ---- the warps' results meet in shared memory, a part of D at a time ----------
 #pragma unroll
-        for (int i = 0; i < ST; ++i) mbar_wait_drain(bars + 8 * i, (phase >> i) & 1u, 10000000ull);
+        for (int ps = 0; ps < L::PASSES; ++ps) {
+            if (ps > 0) __syncthreads();                    // the previous part is read
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int r = nt * 8 + 2 * t4 + e;
+                    if (ps == 0) {
+                        float l = l_run[nt][e];
+                        l += __shfl_xor_sync(0xffffffffu, l, 4);
+                        l += __shfl_xor_sync(0xffffffffu, l, 8);
+                        l += __shfl_xor_sync(0xffffffffu, l, 16);
+                        if (a8 == 0) sml[warp * RW + r] = make_float2(m_run[nt][e], l);
+                    }
+                    // a thread's D / 8 values, of which a part takes D / 8 / PASSES
+                    float* to = so + (static_cast<size_t>(warp) * RW + r) * L::DP + a8 * (L::DP / 8);
+#pragma unroll
+                    for (int mt = 0; mt < MT / L::PASSES; ++mt) {
+                        const float* x = o[nt][ps * (MT / L::PASSES) + mt];
+                        *reinterpret_cast<float2*>(to + mt * 2) = make_float2(x[e], x[e + 2]);
+                    }
+                }
+            }
+            __syncthreads();
+            if (*abort_flag) {                              // waits, which set it, are only before this barrier
+                more = false;
+                break;
+            }
+            for (int idx = threadIdx.x; idx < RW * (L::DP / 4); idx += L::THREADS) {
+                const int r = idx / (L::DP / 4), x4 = idx % (L::DP / 4) * 4;
+                if (row0 + r >= rows) break;
+                const int d = x4 / (L::DP / 8) * (D / 8) + ps * (L::DP / 8) + x4 % (L::DP / 8);
+                float m = -INFINITY;
+#pragma unroll
+                for (int w = 0; w < W; ++w) m = fmaxf(m, sml[w * RW + r].x);
+                float l = 0.f;
+                float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int w = 0; w < W; ++w) {
+                    const float2 ml = sml[w * RW + r];
+                    const float f = merge_weight(ml.x, m);
+                    l += ml.y * f;
+                    const float4 x = *reinterpret_cast<const float4*>(so + (static_cast<size_t>(w) * RW + r) * L::DP + x4);
+                    acc.x += x.x * f;
+                    acc.y += x.y * f;
+                    acc.z += x.z * f;
+                    acc.w += x.w * f;
+                }
+                if (!whole) {
+                    *reinterpret_cast<float4*>(p.part_o + (static_cast<size_t>(slot) * RW + r) * D + d) = acc;
+                    if (d == 0) p.part_ml[static_cast<size_t>(slot) * RW + r] = make_float2(m, l);
+                    continue;
+                }
+                const float inv = out_factor(l);
+                if (p.out_f32)
+                    *reinterpret_cast<float4*>(static_cast<float*>(p.o) + (out_row + r) * D + d) =
+                        make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+                else
+                    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.o) + (out_row + r) * D + d) =
+                        make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+                if (d == 0 && p.lse) p.lse[out_row + r] = row_lse(m, l);
+            }
+        }
+        first_seg = false;
+        if (!more) break;
+        __syncthreads();                                    // the merge buffer is read
     }
-    __syncthreads();
-    float* so = reinterpret_cast<float*>(smem);             // [warps][RW][D]
-    float2* sml = reinterpret_cast<float2*>(smem + L::OFF_ML);   // [warps][16]
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            float l = l_run[nt][e];
-            l += __shfl_xor_sync(0xffffffffu, l, 4);
-            l += __shfl_xor_sync(0xffffffffu, l, 8);
-            l += __shfl_xor_sync(0xffffffffu, l, 16);
-            const int r = nt * 8 + 2 * t4 + e;
-            if (a8 == 0) sml[warp * 16 + r] = make_float2(m_run[nt][e], l);
-            float* to = so + (static_cast<size_t>(warp) * RW + r) * D + a8 * (D / 8);
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
-                *reinterpret_cast<float2*>(to + mt * 2) = make_float2(o[nt][mt][e], o[nt][mt][e + 2]);
-        }
-    }
-    __syncthreads();
-    if (*abort_flag) return;
-    for (int idx = threadIdx.x; idx < RW * (D / 4); idx += kCachedThreads) {
-        const int r = idx / (D / 4), d = idx % (D / 4) * 4;
-        if (row0 + r >= rows) break;
-        float m = -INFINITY;
-#pragma unroll
-        for (int w = 0; w < kCachedWarps; ++w) m = fmaxf(m, sml[w * 16 + r].x);
-        float l = 0.f;
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int w = 0; w < kCachedWarps; ++w) {
-            const float2 ml = sml[w * 16 + r];
-            const float f = merge_weight(ml.x, m);
-            l += ml.y * f;
-            const float4 y = *reinterpret_cast<const float4*>(so + (static_cast<size_t>(w) * RW + r) * D + d);
-            acc.x += y.x * f;
-            acc.y += y.y * f;
-            acc.z += y.z * f;
-            acc.w += y.w * f;
-        }
-        const size_t row = (static_cast<size_t>(s) * p.Hq + static_cast<size_t>(h) * p.G) * p.M + row0 + r;
-        if (p.splits > 1) {
-            *reinterpret_cast<float4*>(p.part_o + (row * p.splits + split) * D + d) = acc;
-            if (d == 0) p.part_ml[row * p.splits + split] = make_float2(m, l);
-            continue;
-        }
-        const float inv = l == 0.f ? 0.f : 1.f / l;
-        if (p.out_f32)
-            *reinterpret_cast<float4*>(static_cast<float*>(p.o) + row * D + d) =
-                make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-        else
-            *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.o) + row * D + d) =
-                make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-        if (d == 0 && p.lse) p.lse[row] = row_lse(m, l);
+    // after an abort, copies still in flight end before the CTA does
+    if (lane == 0 && flying) {
+        for (int i = 0; i < ST; ++i)
+            if ((flying >> i) & 1u) mbar_wait_drain(bars + 8 * i, (phase >> i) & 1u, 1000000000ull);
     }
 }
 
-// Joins the splits of a row, one warp per row, in split order.
-template <int D>
-__global__ void __launch_bounds__(128) cached_combine_kernel(const CachedParams p, long long rows) {
-    const long long row = static_cast<long long>(blockIdx.x) * 4 + warp_id();
-    if (row >= rows) return;
-    const int lane = static_cast<int>(lane_id());
-    const float2* ml = p.part_ml + row * p.splits;
-    float m = -INFINITY;
-    for (int i = lane; i < p.splits; i += 32) m = fmaxf(m, ml[i].x);
+// Joins the parts of the units that a cut divided: slot pieces.x, then those of the following shares' first
+// segments.  One CTA per unit and 8 rows; a warp takes every eighth part.
+template <int D, int NT>
+__global__ void __launch_bounds__(256) cached_combine_kernel(const __grid_constant__ CachedParams p) {
+    constexpr int RW = 8 * NT, PER = D / 32;
+    const int unit = static_cast<int>(blockIdx.x) / NT, r0 = (static_cast<int>(blockIdx.x) - unit * NT) * 8;
+    const int2 pc = p.pieces[unit];
+    if (pc.y <= 0) return;
+    __shared__ float2 top[8];                               // a row's maximum and its sum
+    __shared__ float part[8][8][D];
+    const int warp = static_cast<int>(warp_id()), lane = static_cast<int>(lane_id());
+    const int columns = p.Hkv * p.tiles;
+    auto slot = [&](int i) { return static_cast<size_t>(i == 0 ? pc.x : 2 * (pc.x / 2 + i * columns)) * RW + r0; };
+    {
+        float m = -INFINITY, l = 0.f;
+        for (int i = lane; i < pc.y; i += 32) m = fmaxf(m, p.part_ml[slot(i) + warp].x);
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-    constexpr int PER = D / 32;
-    float acc[PER], l = 0.f;
+        for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+        for (int i = lane; i < pc.y; i += 32) {
+            const float2 y = p.part_ml[slot(i) + warp];
+            l += y.y * merge_weight(y.x, m);
+        }
 #pragma unroll
-    for (int e = 0; e < PER; ++e) acc[e] = 0.f;
-    for (int i = 0; i < p.splits; ++i) {
-        const float2 y = ml[i];
-        const float f = merge_weight(y.x, m);
-        l += y.y * f;
-        const float* src = p.part_o + (row * p.splits + i) * D + lane * PER;
-#pragma unroll
-        for (int e = 0; e < PER; ++e) acc[e] += src[e] * f;
+        for (int off = 16; off > 0; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
+        if (lane == 0) top[warp] = make_float2(m, l);
     }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
+    __syncthreads();
+    float acc[8][PER];
 #pragma unroll
-    for (int e = 0; e < PER; e += 2) {
-        const size_t at = static_cast<size_t>(row) * D + lane * PER + e;
-        if (p.out_f32) *reinterpret_cast<float2*>(static_cast<float*>(p.o) + at) = make_float2(acc[e] * inv, acc[e + 1] * inv);
-        else *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.o) + at) = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
+    for (int r = 0; r < 8; ++r)
+#pragma unroll
+        for (int e = 0; e < PER; ++e) acc[r][e] = 0.f;
+    for (int i = warp; i < pc.y; i += 8) {
+        const float* src = p.part_o + slot(i) * D + lane * PER;
+#pragma unroll
+        for (int r = 0; r < 8; ++r) {
+            const float f = merge_weight(p.part_ml[slot(i) + r].x, top[r].x);
+#pragma unroll
+            for (int e = 0; e < PER; ++e) acc[r][e] += src[r * D + e] * f;
+        }
     }
-    if (lane == 0 && p.lse) p.lse[row] = row_lse(m, l);
+#pragma unroll
+    for (int r = 0; r < 8; ++r)
+#pragma unroll
+        for (int e = 0; e < PER; ++e) part[warp][r][lane * PER + e] = acc[r][e];
+    __syncthreads();
+    const int cell = unit / p.tiles, tile = unit - cell * p.tiles;
+    const int s = cell / p.Hkv, h = cell - s * p.Hkv;
+    const int row0 = tile * RW + r0;
+    const size_t out_row = (static_cast<size_t>(s) * p.Hq + static_cast<size_t>(h) * p.G) * p.M + row0;
+    for (int idx = threadIdx.x; idx < 8 * D / 2; idx += 256) {
+        const int r = idx / (D / 2), d = idx % (D / 2) * 2;
+        if (row0 + r >= p.G * p.M) break;
+        float x0 = 0.f, x1 = 0.f;
+#pragma unroll
+        for (int w = 0; w < 8; ++w) {
+            x0 += part[w][r][d];
+            x1 += part[w][r][d + 1];
+        }
+        const float l = top[r].y, inv = out_factor(l);
+        const size_t at = (out_row + r) * D + d;
+        if (p.out_f32) *reinterpret_cast<float2*>(static_cast<float*>(p.o) + at) = make_float2(x0 * inv, x1 * inv);
+        else *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.o) + at) = pack_bf16x2(x0 * inv, x1 * inv);
+        if (d == 0 && p.lse) p.lse[out_row + r] = row_lse(top[r].x, l);
+    }
 }
 
 }  // namespace calib

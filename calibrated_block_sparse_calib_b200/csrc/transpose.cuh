@@ -2,117 +2,150 @@
 // it.  The gradients of K and V sum over the query blocks of a key block, so they walk this list
 // where the forward pass and the gradient of Q walk the list by query block.
 //
-// One CTA per (head, 32 consecutive key blocks), one launch, no counters and no scan over the
-// list:
-//   - every row's first entry at or past the CTA's columns is found by bisection, since a row is
-//     ascending.  The entries before it, summed over the head's rows, are the entries of all
-//     earlier columns, and a head has as many entries in either order: the CTA's output starts at
-//     row_ptr[h*nq] + that sum.
-//   - the row's entries inside the 32 columns become one 32-bit word, and 32 such words are turned
-//     over by 32 ballots into one word of rows per column, kept in shared memory;
-//   - column counts and their prefix give the new row pointers; one warp per column writes out the
-//     set bits' indices.
-// Integer work in a fixed order: the result is exact and the same in every run.
-// The list is read once per CTA column range only where it has entries, plus about log2(row)
-// probes a row; what bounds a call is the latency of those dependent probes (a 40 x 591 x 591 list
-// at 25%, 3.5 M entries, 14 MB in and out, is 2.2 us of HBM traffic).
+// One CTA per (head, range of key blocks), one launch, no counters and no scan over the list:
+//   - a warp reads a row's entries, sets the bit (column, row) in shared memory for those in the
+//     CTA's range and counts those before it.  A head has as many entries in either order, so the
+//     CTA's output starts at row_ptr[h*nq] + the entries before its range, whatever other CTAs do.
+//   - column counts and their prefix give the new row pointers; one warp per column turns the set
+//     bits into indices, 1024 rows at a time through shared memory, so that they leave in whole lines.
+// Integer work; bits are set in any order and read in one: the result is exact and the same in
+// every run.
+// A row is ascending, so reading stops behind the range.  Rows longer than 512 entries are first
+// narrowed to the 32nd in which the range begins, which costs a dependent probe: up to there reading
+// everything before the range is cheaper (40 x 591 x 591 at 25%, 148 entries a row: 105 us with every
+// row narrowed, 46 us with a bisection by one thread a row, 16 us as it is).
+// What bounds it is the latency of a row's loads, two rows in flight per warp; the 14 MB that a
+// 40 x 591 x 591 list at 25% reads and writes would take 2.2 us of HBM time.
 #pragma once
 #include "ptx.cuh"
 #include "select.cuh"
 
 namespace calib {
 
-constexpr int kTransThreads = 256;
-constexpr int kTransCols = 32;
+constexpr int kTransThreads = 1024;
+constexpr int kTransWarps = kTransThreads / 32;
+constexpr int kTransMaxCols = 128;        // key blocks per CTA, at most
+constexpr int kTransNarrow = 512;
 
 __global__ void __launch_bounds__(kTransThreads)
 transpose_csr_kernel(const int32_t* __restrict__ row_ptr, const int16_t* __restrict__ col_idx, int H, int nq, int nk,
-                     int32_t* __restrict__ t_row_ptr, int16_t* __restrict__ t_col_idx) {
-    extern __shared__ uint32_t colbits[];                 // [kTransCols][words]
-    __shared__ int32_t warp_sum[kTransThreads / 32];
-    __shared__ int32_t count[kTransCols], first[kTransCols];
-    const int tiles = (nk + kTransCols - 1) / kTransCols;
+                     int cols, int32_t* __restrict__ t_row_ptr, int16_t* __restrict__ t_col_idx) {
+    extern __shared__ uint32_t bits[];                    // [cols][stride]: bit i of column c's words = row i keeps it
+    int16_t* stage = reinterpret_cast<int16_t*>(bits + cols * (((nq + 31) / 32) | 1)) + warp_id() * 1024;   // a warp's own
+    __shared__ int32_t warp_sum[kTransWarps];
+    __shared__ int32_t count[kTransMaxCols], first[kTransMaxCols];
+    const int tiles = (nk + cols - 1) / cols;
     const int h = blockIdx.x / tiles;
-    const int j0 = (blockIdx.x - h * tiles) * kTransCols;
-    const int words = (nq + 31) / 32;
+    const int j0 = (blockIdx.x - h * tiles) * cols, j1 = j0 + cols;
+    const int words = (nq + 31) / 32, stride = words | 1;   // odd: neighbouring columns on different banks
     const int warp = static_cast<int>(warp_id()), lane = static_cast<int>(lane_id());
     const int r0 = h * nq;
-    int before = 0;
-    for (int w = warp; w < words; w += kTransThreads / 32) {
-        const int i = w * 32 + lane;
-        uint32_t bits = 0;
-        if (i < nq) {
-            const int beg = row_ptr[r0 + i], end = row_ptr[r0 + i + 1];
-            if (beg < 0 || end < beg || end - beg > nk) {
+    for (int x = threadIdx.x; x < cols * stride; x += kTransThreads) bits[x] = 0u;
+    __syncthreads();
+
+    int before = 0;                                       // this lane's entries before the range
+    auto visit = [&](int c, int i) {
+        if (c < j0) ++before;
+        else if (c < j1) atomicOr(&bits[(c - j0) * stride + (i >> 5)], 1u << (i & 31));
+    };
+    // rows warp, warp + 32, ...: their pointers 32 at a time, one per lane
+    for (int b0 = 0; b0 * kTransWarps < nq; b0 += 32) {
+        int beg_l = 0, end_l = 0;
+        const int il = (b0 + lane) * kTransWarps + warp;
+        if (il < nq) {
+            beg_l = row_ptr[r0 + il];
+            end_l = row_ptr[r0 + il + 1];
+            if (beg_l < 0 || end_l < beg_l || end_l - beg_l > nk) {
                 raise_status(STATUS_BAD_LIST);
-            } else {
-                int lo = beg, hi = end;
-                while (lo < hi) {
-                    const int mid = (lo + hi) >> 1;
-                    if (col_idx[mid] < j0) lo = mid + 1;
-                    else hi = mid;
-                }
-                before += lo - beg;
-                for (; lo < end; ++lo) {
-                    const int c = col_idx[lo] - j0;
-                    if (c >= kTransCols) break;
-                    if (c >= 0) bits |= 1u << c;
-                }
+                beg_l = end_l = 0;
             }
         }
-        uint32_t mine = 0;
+        for (int u = 0; u < 32 && (b0 + u) * kTransWarps + warp < nq; u += 2) {
+            const int i0 = (b0 + u) * kTransWarps + warp, i1 = i0 + kTransWarps;
+            int x0 = __shfl_sync(0xffffffffu, beg_l, u), x1 = __shfl_sync(0xffffffffu, beg_l, u + 1);
+            const int e0 = __shfl_sync(0xffffffffu, end_l, u), e1 = __shfl_sync(0xffffffffu, end_l, u + 1);
+            // of a long row, skip the whole 32nds that lie before the range
+            auto narrow = [&](int& x, int e) {
+                while (e - x > kTransNarrow) {
+                    const long long len = e - x;
+                    const int probe = col_idx[x + static_cast<int>(len * (lane + 1) >> 5) - 1];
+                    const int k = __popc(__ballot_sync(0xffffffffu, probe < j0));
+                    if (k == 0) break;
+                    const int skip = static_cast<int>(len * k >> 5);
+                    if (lane == 0) before += skip;
+                    x += skip;
+                }
+            };
+            narrow(x0, e0);
+            narrow(x1, e1);
+            while (x0 < e0 || x1 < e1) {
+                int c0[2], c1[2];
 #pragma unroll
-        for (int c = 0; c < kTransCols; ++c) {
-            const uint32_t rows = __ballot_sync(0xffffffffu, (bits >> c) & 1u);
-            if (lane == c) mine = rows;
+                for (int v = 0; v < 2; ++v) {
+                    c0[v] = x0 + v * 32 + lane < e0 ? col_idx[x0 + v * 32 + lane] : 0x7fffffff;
+                    c1[v] = x1 + v * 32 + lane < e1 ? col_idx[x1 + v * 32 + lane] : 0x7fffffff;
+                }
+#pragma unroll
+                for (int v = 0; v < 2; ++v) {
+                    visit(c0[v], i0);
+                    visit(c1[v], i1);
+                }
+                // done with a row once its last entry read is behind the range (or its end was met)
+                x0 = __shfl_sync(0xffffffffu, c0[1], 31) >= j1 ? e0 : x0 + 64;
+                x1 = __shfl_sync(0xffffffffu, c1[1], 31) >= j1 ? e1 : x1 + 64;
+            }
         }
-        colbits[lane * words + w] = mine;
     }
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) before += __shfl_xor_sync(0xffffffffu, before, off);
     if (lane == 0) warp_sum[warp] = before;
     __syncthreads();
-    for (int c = warp; c < kTransCols; c += kTransThreads / 32) {
+    for (int c = warp; c < cols; c += kTransWarps) {
         int n = 0;
-        for (int w = lane; w < words; w += 32) n += __popc(colbits[c * words + w]);
+        for (int w = lane; w < words; w += 32) n += __popc(bits[c * stride + w]);
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1) n += __shfl_xor_sync(0xffffffffu, n, off);
         if (lane == 0) count[c] = n;
     }
     __syncthreads();
     if (warp == 0) {
-        int at = row_ptr[r0];
-#pragma unroll
-        for (int w = 0; w < kTransThreads / 32; ++w) at += warp_sum[w];
-        int incl = count[lane];
-#pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, incl, off);
-            if (lane >= off) incl += y;
-        }
-        first[lane] = at + incl - count[lane];
-        if (j0 + lane < nk) t_row_ptr[static_cast<size_t>(h) * nk + j0 + lane + 1] = at + incl;
+        int at = row_ptr[r0] + __reduce_add_sync(0xffffffffu, warp_sum[lane]);
         if (blockIdx.x == 0 && lane == 0) t_row_ptr[0] = at;
+        for (int c = lane; c < cols; c += 32) {
+            int incl = count[c];
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, incl, off);
+                if (lane >= off) incl += y;
+            }
+            first[c] = at + incl - count[c];
+            if (j0 + c < nk) t_row_ptr[static_cast<size_t>(h) * nk + j0 + c + 1] = at + incl;
+            at += __shfl_sync(0xffffffffu, incl, 31);
+        }
     }
     __syncthreads();
-    for (int c = warp; c < kTransCols; c += kTransThreads / 32) {
+    for (int c = warp; c < cols; c += kTransWarps) {
         int out = first[c];
         for (int w0 = 0; w0 < words; w0 += 32) {
-            uint32_t bits = w0 + lane < words ? colbits[c * words + w0 + lane] : 0u;
-            const int n = __popc(bits);
+            uint32_t word = w0 + lane < words ? bits[c * stride + w0 + lane] : 0u;
+            const int n = __popc(word);
             int incl = n;
 #pragma unroll
             for (int off = 1; off < 32; off <<= 1) {
                 const int y = __shfl_up_sync(0xffffffffu, incl, off);
                 if (lane >= off) incl += y;
             }
-            int o = out + incl - n;
-            while (bits) {
-                const int b = __ffs(bits) - 1;
-                bits &= bits - 1;
-                t_col_idx[o++] = static_cast<int16_t>((w0 + lane) * 32 + b);
+            int o = incl - n;
+            while (word) {
+                const int b = __ffs(word) - 1;
+                word &= word - 1;
+                stage[o++] = static_cast<int16_t>((w0 + lane) * 32 + b);
             }
-            out += __shfl_sync(0xffffffffu, incl, 31);
+            __syncwarp();
+            const int total = __shfl_sync(0xffffffffu, incl, 31);
+            for (int x = lane; x < total; x += 32) t_col_idx[out + x] = stage[x];
+            __syncwarp();
+            out += total;
         }
     }
 }
