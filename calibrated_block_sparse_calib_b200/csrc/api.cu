@@ -98,6 +98,34 @@ bool make_tmap(CUtensorMap* map, const void* base, int D, int N, int H, int box_
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// One launch with what a <<<>>> launch cannot say: a cluster size, or (overlap) that the kernel may begin while
+// the stream's previous kernel ends; it then waits itself before it reads that one's results.
+template <class... P, class... A>
+calib_status launch_with(void (*fn)(P...), int grid, int threads, int smem, cudaStream_t st, int cluster, bool overlap,
+                         const A&... args) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    int n = 0;
+    if (cluster > 1) {
+        attr[n].id = cudaLaunchAttributeClusterDimension;
+        attr[n].val.clusterDim.x = cluster;
+        attr[n].val.clusterDim.y = attr[n].val.clusterDim.z = 1;
+        ++n;
+    }
+    if (overlap) {
+        attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[n].val.programmaticStreamSerializationAllowed = 1;
+        ++n;
+    }
+    cfg.attrs = attr;
+    cfg.numAttrs = n;
+    return cudaLaunchKernelEx(&cfg, fn, args...) == cudaSuccess ? CALIB_OK : (cudaGetLastError(), CALIB_ERR_CUDA);
+}
+
 calib_status launch_status() {
     return cudaGetLastError() == cudaSuccess ? CALIB_OK : CALIB_ERR_CUDA;
 }
@@ -334,8 +362,7 @@ calib_status launch_bwd(const calib::BwdMaps& m, const calib::BwdParams& p, cuda
     if (calib_status s = ensure_smem(reinterpret_cast<const void*>(fn), L::BYTES)) return s;
     calib::bwd_prepare_kernel<D><<<static_cast<int>((threads + 255) / 256), 256, 0, st>>>(p, rows);
     if (calib_status s = launch_status()) return s;
-    fn<<<p.geo.H * (p.geo.nk + p.geo.nq), calib::kBwdThreads, L::BYTES, st>>>(m, p);
-    return launch_status();
+    return launch_with(fn, p.geo.H * (p.geo.nk + p.geo.nq), calib::kBwdThreads, L::BYTES, st, 1, true, m, p);
 }
 
 calib_status bwd_common(const void* q, const void* k, const void* v, const void* o, const void* dout,
@@ -401,12 +428,13 @@ calib_status bwd_common(const void* q, const void* k, const void* v, const void*
 constexpr int kSms = 148;
 
 // How a call's work is shared (see cached_attn_kernel): rows per unit (8 or 16), units per K/V head, and `flat`:
-// shares per K/V head and row tile, or 0 for a CTA per unit.  Own CTAs, and no second launch, where no sequence can
-// be longer than 2048 keys (5 to 8 steps for each of a CTA's warps, about what the cut's merge costs) or the units
-// fill the GPU 8 times and more.  The shares fill the GPU's places once, or twice where once would leave more
-// than a tenth of them empty.
+// shares per K/V head and row tile, or 0 for a cluster per unit and no second launch.  Clusters where no sequence
+// can be longer than 2048 keys (5 to 8 steps for each of a CTA's warps, about what the cut's merge costs), or
+// 8192 if the GPU has room for clusters of 8, or where the units fill the GPU 8 times and more; a cluster has one step
+// for each of its warps, as far as 8 CTAs and the GPU's places go.  The shares fill the GPU's places once, or twice
+// where once would leave more than a tenth of them empty.
 struct CachedPlan {
-    int nt, tiles, flat;
+    int nt, tiles, flat, cluster;
     long long units, grid;
     int64_t part_o, part_ml, bytes;   // workspace: offsets of the parts and their statistics; `pieces` is at 0
 };
@@ -420,7 +448,13 @@ CachedPlan cached_plan(int S, int Hq, int Hkv, int M, int D, int B, int nb) {
     c.grid = c.units;
     const long long places = kSms * (D == 128 ? 1 : 2);
     const long long keys = static_cast<long long>(nb) * B;
-    if (keys > 2048 && c.units < 8 * places) {
+    c.cluster = 1;
+    if (c.units >= 8 * places) return c;
+    if (keys <= 2048 || (keys <= 8192 && c.units * 8 <= places)) {
+        const int warps = D == 128 && c.nt == 1 ? 12 : 8;
+        while (c.cluster < 8 && c.cluster * warps < keys / calib::kChunk && c.units * c.cluster * 2 <= places) c.cluster *= 2;
+        c.grid = c.units * c.cluster;
+    } else {
         long long shares = std::max(1ll, places / columns);
         if (shares * columns * 10 < places * 9) shares = std::max(1ll, 2 * places / columns);
         const long long total = S * (keys / calib::kChunk + calib::kUnitCost);
@@ -471,11 +505,10 @@ calib_status launch_cached(const CUtensorMap& tk, const CUtensorMap& tv, const c
     static_assert(L::BYTES <= 232448 / L::CTAS - (L::CTAS > 1 ? 1024 : 0), "shared memory budget");
     auto* fn = calib::cached_attn_kernel<D, B, NT>;
     if (calib_status s = ensure_smem(reinterpret_cast<const void*>(fn), L::BYTES)) return s;
-    fn<<<static_cast<int>(c.grid), L::THREADS, L::BYTES, st>>>(tk, tv, p);
-    if (calib_status s = launch_status()) return s;
+    if (calib_status s = launch_with(fn, static_cast<int>(c.grid), L::THREADS, L::BYTES, st, p.cluster, false, tk, tv, p))
+        return s;
     if (!p.flat) return CALIB_OK;
-    calib::cached_combine_kernel<D, NT><<<static_cast<int>(c.units) * NT, 256, 0, st>>>(p);
-    return launch_status();
+    return launch_with(calib::cached_combine_kernel<D, NT>, static_cast<int>(c.units) * NT, 256, 0, st, 1, true, p);
 }
 
 template <int D, int B>
@@ -673,14 +706,12 @@ calib_status calib_transpose_csr(const int32_t* row_ptr, const int16_t* col_idx,
     if (H < 1 || nq < 1 || nk < 1 || nq > 32767 || nk > 32767) return CALIB_ERR_INVALID;
     if (static_cast<long long>(H) * std::max(nq, nk) > (1ll << 31) - 2) return CALIB_ERR_INVALID;
     if (calib_status s = check_device()) return s;
-    // 128 key blocks per CTA while their bits leave room for two CTAs on an SM (up to about 3000 query blocks),
+    // 128 key blocks per CTA while their bits leave room for two CTAs on an SM (up to about 6900 query blocks),
     // 32 beyond (131 KB at the most query blocks)
     const int stride = cdiv(nq, 32) | 1;
-    const int cols = calib::kTransMaxCols * stride * 4 <= 48 * 1024 ? calib::kTransMaxCols : 32;
-    const int bytes = cols * stride * 4 + calib::kTransWarps * 1024 * 2;
-    if (calib_status s = ensure_smem(reinterpret_cast<const void*>(calib::transpose_csr_kernel),
-                                     32 * 1025 * 4 + calib::kTransWarps * 1024 * 2))
-        return s;
+    const int cols = calib::kTransMaxCols * stride * 4 <= 110 * 1024 ? calib::kTransMaxCols : 32;
+    const int bytes = cols * stride * 4;
+    if (calib_status s = ensure_smem(reinterpret_cast<const void*>(calib::transpose_csr_kernel), 32 * 1025 * 4)) return s;
     calib::transpose_csr_kernel<<<H * cdiv(nk, cols), calib::kTransThreads, bytes, as_stream(stream)>>>(
         row_ptr, col_idx, H, nq, nk, cols, t_row_ptr_out, t_col_idx_out);
     return launch_status();
@@ -759,7 +790,7 @@ calib_status sparse_attn_cached(const void* q, const void* k_cache, const void* 
         p.part_ml = reinterpret_cast<float2*>(base + c.part_ml);
     }
     p.S = S; p.Hq = Hq; p.Hkv = Hkv; p.G = Hq / Hkv; p.M = M; p.nb = max_blocks; p.pages = static_cast<int>(pages);
-    p.tiles = c.tiles; p.flat = c.flat;
+    p.tiles = c.tiles; p.flat = c.flat; p.cluster = c.cluster;
     p.causal = (flags & CALIB_ATTN_CAUSAL) ? 1 : 0;
     p.out_f32 = (flags & CALIB_ATTN_OUT_F32) ? 1 : 0;
     p.scale_log2 = scale * 1.4426950408889634f;

@@ -258,7 +258,10 @@ __device__ __forceinline__ void bwd_kv(const BwdMaps& m, const BwdParams& p, int
     const uint32_t warp = warp_id(), lane = lane_id();
 
     int h, j, beg, n;
-    if (!bwd_item(id, p.t_work, p.t_row_ptr, g.nk, g.nq, g.H, &h, &j, &beg, &n)) return;
+    if (!bwd_item(id, p.t_work, p.t_row_ptr, g.nk, g.nq, g.H, &h, &j, &beg, &n)) {
+        wait_for_previous_launch();
+        return;
+    }
     const bool rep = repeats(g, h);
 
     if (threadIdx.x == 0) {
@@ -287,6 +290,7 @@ __device__ __forceinline__ void bwd_kv(const BwdMaps& m, const BwdParams& p, int
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    wait_for_previous_launch();                            // bwd_prepare_kernel's results
     const uint32_t tmem = *tmem_slot;
     const WaitCtl ctl{abort_flag, p.timeout_ns};
     int armed_r = 0, armed = 0, armed_b = 0;
@@ -550,10 +554,16 @@ __device__ __forceinline__ void bwd_q(const BwdMaps& m, const BwdParams& p, int 
     const uint32_t warp = warp_id(), lane = lane_id();
 
     int h, i, beg, n;
-    if (!bwd_item(id, p.work, p.row_ptr, g.nq, g.nk, g.H, &h, &i, &beg, &n)) return;
+    if (!bwd_item(id, p.work, p.row_ptr, g.nq, g.nk, g.H, &h, &i, &beg, &n)) {
+        wait_for_previous_launch();
+        return;
+    }
     const bool rep = repeats(g, h);
     const int Nq = rep ? g.n_anchor : g.N;
-    if (i * BLK >= Nq) return;                             // rows past the anchor space
+    if (i * BLK >= Nq) {                                   // rows past the anchor space
+        wait_for_previous_launch();
+        return;
+    }
 
     if (threadIdx.x == 0) {
         mbar_init(bar(L::B_R), 1);
@@ -580,6 +590,7 @@ __device__ __forceinline__ void bwd_q(const BwdMaps& m, const BwdParams& p, int 
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    wait_for_previous_launch();                            // bwd_prepare_kernel's results
     const uint32_t tmem = *tmem_slot;
     const WaitCtl ctl{abort_flag, p.timeout_ns};
     int armed_r = 0, armed = 0, armed_b = 0;

@@ -77,15 +77,8 @@ __global__ void __launch_bounds__(kWriteThreads) cache_write_kernel(const CacheW
     const int start = len - n_new;                         // first new position
     const int blk = start / B + t;
     if (n_new == 0 || static_cast<long long>(blk) * B >= len) return;
-    const int page = p.table[static_cast<size_t>(s) * p.nb + blk];
-    if (page < 0 || page >= p.pages) {
-        if (threadIdx.x == 0) raise_status(STATUS_BAD_CACHE);
-        return;
-    }
+    const int page = p.table[static_cast<size_t>(s) * p.nb + blk];   // used after the new tokens are on their way
     const int lo = max(start - blk * B, 0), hi = min(len - blk * B, B);    // new tokens [lo, hi) of the block
-    const size_t cell = static_cast<size_t>(page) * p.Hkv + h;
-    uint8_t* data = (is_v ? p.v : p.k) + cell * B * D;
-    float* scale_at = (is_v ? p.v_scale : p.k_scale) + cell;
     const __nv_bfloat16* src = (is_v ? p.v_new : p.k_new) +
                                (static_cast<size_t>(s) * p.Hkv + h) * p.M * D +
                                (static_cast<long long>(blk) * B - start) * D;   // token 0 of the block, if it were new
@@ -97,6 +90,17 @@ __global__ void __launch_bounds__(kWriteThreads) cache_write_kernel(const CacheW
         const int tok = idx / CPR;
         raw[c] = make_uint4(0, 0, 0, 0);
         if (tok >= lo && tok < hi) raw[c] = *reinterpret_cast<const uint4*>(src + static_cast<long long>(tok) * D + idx % CPR * 8);
+    }
+    if (page < 0 || page >= p.pages) {
+        if (threadIdx.x == 0) raise_status(STATUS_BAD_CACHE);
+        return;
+    }
+    const size_t cell = static_cast<size_t>(page) * p.Hkv + h;
+    uint8_t* data = (is_v ? p.v : p.k) + cell * B * D;
+    float* scale_at = (is_v ? p.v_scale : p.k_scale) + cell;
+    const float held = lo > 0 ? *scale_at : 0.f;
+#pragma unroll
+    for (int c = 0; c < PER; ++c) {
         const uint32_t w[4] = {raw[c].x, raw[c].y, raw[c].z, raw[c].w};
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -107,7 +111,6 @@ __global__ void __launch_bounds__(kWriteThreads) cache_write_kernel(const CacheW
     }
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
-    const float held = lo > 0 ? *scale_at : 0.f;
     if (lane_id() == 0) red[warp_id()] = amax;
     __syncthreads();
 #pragma unroll
@@ -167,7 +170,8 @@ struct CachedParams {
     float2* part_ml;                      // workspace [2 grid][RW]
     int2* pieces;                         // workspace [units]: first slot, count (0: written already)
     int S, Hq, Hkv, G, M, nb, pages, tiles, causal, out_f32;
-    int flat;                             // shares per K/V head and row tile, or 0: a CTA per unit
+    int flat;                             // shares per K/V head and row tile, or 0: a cluster per unit
+    int cluster;                          // CTAs per cluster (1 with flat)
     float scale_log2;
     uint64_t timeout_ns;
 };
@@ -285,6 +289,26 @@ __device__ __forceinline__ CachedCell cached_cell(const CachedParams& p, int s, 
     return c;
 }
 
+// Clusters: rank and size, a barrier over all their threads (each thread's earlier shared-memory writes are
+// seen after it), and a load from the same address in another CTA's shared memory.
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_barrier() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ float4 cluster_load(uint32_t addr, uint32_t rank) {
+    float4 v;
+    asm volatile("{\n\t.reg .u32 a;\n\tmapa.shared::cluster.u32 a, %4, %5;\n\t"
+                 "ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [a];\n\t}"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr), "r"(rank)
+                 : "memory");
+    return v;
+}
+
 // Attention of a few query rows over a sequence's cached keys: the G query heads of a K/V head
 // times M query tokens are the rows, 8 * NT of them per unit (a cell and a tile of its rows).
 //
@@ -298,8 +322,9 @@ __device__ __forceinline__ CachedCell cached_cell(const CachedParams& p, int s, 
 // ones.  A unit that a cut divides leaves its parts in the workspace for cached_combine_kernel.  The heads' cuts
 // fall on the same places, and CTAs with the same share are neighbours, so the heads of a page, which lie side by
 // side in memory, are read at the same time (4 x 131072 tokens, 8 heads: 216 us with one line through all heads
-// on 148 SMs, 190 us with the heads side by side on 128).  Otherwise one CTA per unit and no second launch: where a
-// sequence is short, or the units fill the GPU several times anyway.
+// on 148 SMs, 170 us with the heads side by side).  Otherwise a cluster of CTAs per unit (its chunks cut evenly,
+// the results joined through distributed shared memory) and no second launch: where sequences are short, or the
+// units fill the GPU several times anyway (a cluster is then one CTA).
 //
 // Rows are few, so they are the N of the products and the keys their M: S^T = K Q^T and
 // O^T = V^T P^T as 16x8x16 MMAs, which wastes nothing at 8 rows where rows as M would fill half of a
@@ -351,9 +376,10 @@ cached_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
     long long total = 0, left = 0, pos = 0;                 // flat: of the column; of the share; where it stands
     int shares = 1, share = 0, v0 = 0;                      // v0: position in the unit (chunks, then its own cost)
     int seq = 0;
-    const int column = static_cast<int>(blockIdx.x) % columns, tile = column % p.tiles, head = column / p.tiles;
+    const int unit0 = static_cast<int>(blockIdx.x) / p.cluster;
+    const int column = unit0 % columns, tile = column % p.tiles, head = column / p.tiles;
     if (p.flat) {
-        share = static_cast<int>(blockIdx.x) / columns;
+        share = unit0 / columns;
         const int per = (p.S + L::THREADS - 1) / L::THREADS;
         const int lo = min(p.S, static_cast<int>(threadIdx.x) * per), hi = min(p.S, lo + per);
         long long mine = 0;
@@ -390,7 +416,7 @@ cached_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
         seq = start[0];
         v0 = start[1];
     } else {
-        seq = static_cast<int>(blockIdx.x) / columns;
+        seq = unit0 / columns;
         __syncthreads();
     }
 
@@ -412,6 +438,11 @@ cached_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
         cut();
         return true;
     };
+    const int rank = p.cluster > 1 ? static_cast<int>(cluster_rank()) : 0;
+    if (p.cluster > 1) {
+        c0 = cl.chunks * rank / p.cluster;
+        c1 = cl.chunks * (rank + 1) / p.cluster;
+    }
     if (p.flat) {
         cut();
         if (v0 > 0 && c0 == c1 && !next_unit()) return;     // the share begins in a unit's own cost: nothing to do there
@@ -477,6 +508,16 @@ cached_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
     const int vk0 = 2 * t4, vk1 = (2 * t4 + 1) ^ 4;         // keys of MMA rows 2 t4, 2 t4 + 1
     const int rows = p.G * p.M;
     bool ok = true;
+    auto put_out = [&](size_t row, int d, float4 acc, float m, float l) {
+        const float inv = out_factor(l);
+        if (p.out_f32)
+            *reinterpret_cast<float4*>(static_cast<float*>(p.o) + row * D + d) =
+                make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+        else
+            *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.o) + row * D + d) =
+                make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+        if (d == 0 && p.lse) p.lse[row] = row_lse(m, l);
+    };
     while (true) {
         // ---- Q: rows a8 + 8 nt, scaled by a power of two, as the B operand -------
         const int row0 = tile * RW;
@@ -760,24 +801,48 @@ cached_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                     acc.z += x.z * f;
                     acc.w += x.w * f;
                 }
+                if (p.cluster > 1) {                        // the ring's loads are all used: the CTA's result goes there
+                    *reinterpret_cast<float4*>(smem + (r * D + d) * 4) = acc;
+                    if (d == 0) *reinterpret_cast<float4*>(smem + RW * D * 4 + r * 16) = make_float4(m, l, 0.f, 0.f);
+                    continue;
+                }
                 if (!whole) {
                     *reinterpret_cast<float4*>(p.part_o + (static_cast<size_t>(slot) * RW + r) * D + d) = acc;
                     if (d == 0) p.part_ml[static_cast<size_t>(slot) * RW + r] = make_float2(m, l);
                     continue;
                 }
-                const float inv = out_factor(l);
-                if (p.out_f32)
-                    *reinterpret_cast<float4*>(static_cast<float*>(p.o) + (out_row + r) * D + d) =
-                        make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-                else
-                    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.o) + (out_row + r) * D + d) =
-                        make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-                if (d == 0 && p.lse) p.lse[out_row + r] = row_lse(m, l);
+                put_out(out_row + r, d, acc, m, l);
             }
         }
         first_seg = false;
         if (!more) break;
         __syncthreads();                                    // the merge buffer is read
+    }
+    // ---- a cluster's results: each CTA reads a part of all of them ----------------
+    if (p.cluster > 1) {
+        cluster_barrier();
+        const uint32_t base = smem_u32(smem);
+        const int row0 = tile * RW;
+        const size_t out_row = (static_cast<size_t>(cl.s) * p.Hq + static_cast<size_t>(cl.h) * p.G) * p.M + row0;
+        for (int idx = rank * L::THREADS + threadIdx.x; idx < RW * (D / 4) && !*abort_flag; idx += p.cluster * L::THREADS) {
+            const int r = idx / (D / 4), d = idx % (D / 4) * 4;
+            if (row0 + r >= rows) break;
+            float m = -INFINITY, l = 0.f;
+            for (int c = 0; c < p.cluster; ++c) m = fmaxf(m, cluster_load(base + RW * D * 4 + r * 16, c).x);
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int c = 0; c < p.cluster; ++c) {
+                const float4 ml = cluster_load(base + RW * D * 4 + r * 16, c);
+                const float4 x = cluster_load(base + (r * D + d) * 4, c);
+                const float f = merge_weight(ml.x, m);
+                l += ml.y * f;
+                acc.x += x.x * f;
+                acc.y += x.y * f;
+                acc.z += x.z * f;
+                acc.w += x.w * f;
+            }
+            put_out(out_row + r, d, acc, m, l);
+        }
+        cluster_barrier();                                  // no CTA ends while another reads its results
     }
     // after an abort, copies still in flight end before the CTA does
     if (lane == 0 && flying) {
@@ -791,6 +856,7 @@ cached_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
 template <int D, int NT>
 __global__ void __launch_bounds__(256) cached_combine_kernel(const __grid_constant__ CachedParams p) {
     constexpr int RW = 8 * NT, PER = D / 32;
+    wait_for_previous_launch();
     const int unit = static_cast<int>(blockIdx.x) / NT, r0 = (static_cast<int>(blockIdx.x) - unit * NT) * 8;
     const int2 pc = p.pieces[unit];
     if (pc.y <= 0) return;

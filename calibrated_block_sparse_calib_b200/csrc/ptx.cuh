@@ -47,6 +47,9 @@ __device__ __forceinline__ bool elect_one() {
 }
 __device__ __forceinline__ uint32_t warp_id() { return threadIdx.x >> 5; }
 
+// A kernel launched to begin while the one before it ends: waits until that one is done and its writes are seen.
+__device__ __forceinline__ void wait_for_previous_launch() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // ------------------------------------------------------------------------------------
 // mbarrier
 // ------------------------------------------------------------------------------------

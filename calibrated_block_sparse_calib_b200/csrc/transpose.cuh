@@ -6,8 +6,8 @@
 //   - a warp reads a row's entries, sets the bit (column, row) in shared memory for those in the
 //     CTA's range and counts those before it.  A head has as many entries in either order, so the
 //     CTA's output starts at row_ptr[h*nq] + the entries before its range, whatever other CTAs do.
-//   - column counts and their prefix give the new row pointers; one warp per column turns the set
-//     bits into indices, 1024 rows at a time through shared memory, so that they leave in whole lines.
+//   - column counts and their prefix give the new row pointers; one warp per column writes out the
+//     set bits' indices, a word's 32 rows at a time, side by side.
 // Integer work; bits are set in any order and read in one: the result is exact and the same in
 // every run.
 // A row is ascending, so reading stops behind the range.  Rows longer than 512 entries are first
@@ -31,16 +31,15 @@ __global__ void __launch_bounds__(kTransThreads)
 transpose_csr_kernel(const int32_t* __restrict__ row_ptr, const int16_t* __restrict__ col_idx, int H, int nq, int nk,
                      int cols, int32_t* __restrict__ t_row_ptr, int16_t* __restrict__ t_col_idx) {
     extern __shared__ uint32_t bits[];                    // [cols][stride]: bit i of column c's words = row i keeps it
-    int16_t* stage = reinterpret_cast<int16_t*>(bits + cols * (((nq + 31) / 32) | 1)) + warp_id() * 1024;   // a warp's own
     __shared__ int32_t warp_sum[kTransWarps];
     __shared__ int32_t count[kTransMaxCols], first[kTransMaxCols];
     const int tiles = (nk + cols - 1) / cols;
     const int h = blockIdx.x / tiles;
-    const int j0 = (blockIdx.x - h * tiles) * cols, j1 = j0 + cols;
+    const int j0 = (blockIdx.x - h * tiles) * cols, j1 = min(nk, j0 + cols), n_cols = j1 - j0;
     const int words = (nq + 31) / 32, stride = words | 1;   // odd: neighbouring columns on different banks
     const int warp = static_cast<int>(warp_id()), lane = static_cast<int>(lane_id());
     const int r0 = h * nq;
-    for (int x = threadIdx.x; x < cols * stride; x += kTransThreads) bits[x] = 0u;
+    for (int x = threadIdx.x; x < n_cols * stride; x += kTransThreads) bits[x] = 0u;
     __syncthreads();
 
     int before = 0;                                       // this lane's entries before the range
@@ -100,7 +99,7 @@ transpose_csr_kernel(const int32_t* __restrict__ row_ptr, const int16_t* __restr
     for (int off = 16; off > 0; off >>= 1) before += __shfl_xor_sync(0xffffffffu, before, off);
     if (lane == 0) warp_sum[warp] = before;
     __syncthreads();
-    for (int c = warp; c < cols; c += kTransWarps) {
+    for (int c = warp; c < n_cols; c += kTransWarps) {
         int n = 0;
         for (int w = lane; w < words; w += 32) n += __popc(bits[c * stride + w]);
 #pragma unroll
@@ -111,41 +110,28 @@ transpose_csr_kernel(const int32_t* __restrict__ row_ptr, const int16_t* __restr
     if (warp == 0) {
         int at = row_ptr[r0] + __reduce_add_sync(0xffffffffu, warp_sum[lane]);
         if (blockIdx.x == 0 && lane == 0) t_row_ptr[0] = at;
-        for (int c = lane; c < cols; c += 32) {
-            int incl = count[c];
+        for (int c0 = 0; c0 < n_cols; c0 += 32) {
+            const int c = c0 + lane, own = c < n_cols ? count[c] : 0;
+            int incl = own;
 #pragma unroll
             for (int off = 1; off < 32; off <<= 1) {
                 const int y = __shfl_up_sync(0xffffffffu, incl, off);
                 if (lane >= off) incl += y;
             }
-            first[c] = at + incl - count[c];
-            if (j0 + c < nk) t_row_ptr[static_cast<size_t>(h) * nk + j0 + c + 1] = at + incl;
+            if (c < n_cols) {
+                first[c] = at + incl - own;
+                t_row_ptr[static_cast<size_t>(h) * nk + j0 + c + 1] = at + incl;
+            }
             at += __shfl_sync(0xffffffffu, incl, 31);
         }
     }
     __syncthreads();
-    for (int c = warp; c < cols; c += kTransWarps) {
+    for (int c = warp; c < n_cols; c += kTransWarps) {
         int out = first[c];
-        for (int w0 = 0; w0 < words; w0 += 32) {
-            uint32_t word = w0 + lane < words ? bits[c * stride + w0 + lane] : 0u;
-            const int n = __popc(word);
-            int incl = n;
-#pragma unroll
-            for (int off = 1; off < 32; off <<= 1) {
-                const int y = __shfl_up_sync(0xffffffffu, incl, off);
-                if (lane >= off) incl += y;
-            }
-            int o = incl - n;
-            while (word) {
-                const int b = __ffs(word) - 1;
-                word &= word - 1;
-                stage[o++] = static_cast<int16_t>((w0 + lane) * 32 + b);
-            }
-            __syncwarp();
-            const int total = __shfl_sync(0xffffffffu, incl, 31);
-            for (int x = lane; x < total; x += 32) t_col_idx[out + x] = stage[x];
-            __syncwarp();
-            out += total;
+        for (int w = 0; w < words; ++w) {
+            const uint32_t word = bits[c * stride + w];
+            if ((word >> lane) & 1u) t_col_idx[out + __popc(word & lanemask_lt())] = static_cast<int16_t>(w * 32 + lane);
+            out += __popc(word);
         }
     }
 }
