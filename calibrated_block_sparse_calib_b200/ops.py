@@ -110,9 +110,11 @@ def _ptr(t: Optional[torch.Tensor]):
 
 def _need(t: torch.Tensor, name: str, dtype: torch.dtype, shape=None):
     # a small call's time is mostly its checks: the usual case is decided by one expression
-    if (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype and t.is_contiguous()
-            and (shape is None or t.shape == shape)):
-        return
+    try:
+        if t.is_cuda and t.dtype is dtype and t.is_contiguous() and (shape is None or t.shape == shape):
+            return
+    except AttributeError:
+        pass
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.dtype != dtype:
@@ -284,7 +286,7 @@ def transpose_csr(row_ptr: torch.Tensor, col_idx: torch.Tensor, H: int, nq: int,
     _need(row_ptr, "row_ptr", torch.int32, (H * nq + 1,))
     _need(col_idx, "col_idx", torch.int16)
     _on_current_device(row_ptr, col_idx)
-    t_ptr = torch.empty(H * nk + 1, dtype=torch.int32, device=row_ptr.device)
+    t_ptr = row_ptr.new_empty(H * nk + 1)
     t_col = torch.empty_like(col_idx)
     # an empty list still needs valid pointers
     src, dst = (col_idx, t_col) if col_idx.numel() else (row_ptr, t_ptr)
@@ -491,24 +493,36 @@ def sparse_attn_fwd_repeat(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, bl
 # ----------------------------------------------------------------------------------
 
 def _bwd(name, q, k, v, out, dout, lse, blist, blist_t, scale, grads, grad_dtype, n_anchor, geometry):
-    H, N, D = q.shape
-    for t, n in ((q, "q"), (k, "k"), (v, "v")):
-        _need(t, n, torch.bfloat16, (H, N, D))
-    if out.dtype not in (torch.bfloat16, torch.float32):
+    H, N, D = shape = q.shape
+    _need(q, "q", torch.bfloat16)
+    _need(k, "k", torch.bfloat16, shape)
+    _need(v, "v", torch.bfloat16, shape)
+    io = out.dtype
+    if io is not torch.bfloat16 and io is not torch.float32:
         raise TypeError("out must be bf16 or fp32")
-    _need(out, "out", out.dtype, (H, N, D))
-    _need(dout, "dout", out.dtype, (H, N, D))
+    _need(out, "out", io, shape)
+    _need(dout, "dout", io, shape)
     _need(lse, "lse", torch.float32, (H, N))
-    if grad_dtype not in (torch.bfloat16, torch.float32):
+    if grad_dtype is not torch.bfloat16 and grad_dtype is not torch.float32:
         raise TypeError("gradients are bf16 or fp32")
-    dq, dk, dv = (torch.empty((H, N, D), dtype=grad_dtype, device=q.device) if t is None else t for t in grads)
-    for t, n in ((dq, "dq"), (dk, "dk"), (dv, "dv")):
-        _need(t, n, grad_dtype, (H, N, D))
+    dq, dk, dv = grads
+    if dq is None:
+        dq = torch.empty_like(q, dtype=grad_dtype)
+    else:
+        _need(dq, "dq", grad_dtype, shape)
+    if dk is None:
+        dk = torch.empty_like(q, dtype=grad_dtype)
+    else:
+        _need(dk, "dk", grad_dtype, shape)
+    if dv is None:
+        dv = torch.empty_like(q, dtype=grad_dtype)
+    else:
+        _need(dv, "dv", grad_dtype, shape)
     if blist_t is None:
         blist_t = blist.transpose()
     _on_current_device(q, k, v, out, dout, lse, dq, dk, dv, blist.row_ptr, blist_t.row_ptr)
-    flags = (CALIB_ATTN_OUT_F32 if out.dtype == torch.float32 else 0) | \
-        (CALIB_ATTN_GRAD_F32 if grad_dtype == torch.float32 else 0)
+    flags = (CALIB_ATTN_OUT_F32 if io is torch.float32 else 0) | \
+        (CALIB_ATTN_GRAD_F32 if grad_dtype is torch.float32 else 0)
     need = _workspace_bytes("sparse_attn_bwd_workspace", H, N, D, blist.block, n_anchor, flags)
     space = torch.empty(max(1, need), dtype=torch.uint8, device=q.device)
     cs, ct = blist.c_struct(), blist_t.c_struct()
@@ -605,9 +619,9 @@ class KVCache:
 
     def check(self):
         """(pages, Hkv, block, D) of a well-formed cache; raises otherwise."""
-        pages, Hkv, block, D = self.k.shape
+        pages, Hkv, block, D = shape = self.k.shape
         _need(self.k, "cache.k", torch.float8_e4m3fn)
-        _need(self.v, "cache.v", torch.float8_e4m3fn, self.k.shape)
+        _need(self.v, "cache.v", torch.float8_e4m3fn, shape)
         _need(self.k_scale, "cache.k_scale", torch.float32, (pages, Hkv))
         _need(self.v_scale, "cache.v_scale", torch.float32, (pages, Hkv))
         return pages, Hkv, block, D
@@ -629,8 +643,9 @@ def cache_write(cache: KVCache, k_new: torch.Tensor, v_new: torch.Tensor, block_
     sequence s goes to position lengths[s] - new_lens[s] + m (new_lens: M each by default)."""
     pages, Hkv, block, D = cache.check()
     S, M = k_new.shape[0], k_new.shape[2] if k_new.dim() == 4 else 0
-    _need(k_new, "k_new", torch.bfloat16, (S, Hkv, M, D))
-    _need(v_new, "v_new", torch.bfloat16, (S, Hkv, M, D))
+    shape = (S, Hkv, M, D)
+    _need(k_new, "k_new", torch.bfloat16, shape)
+    _need(v_new, "v_new", torch.bfloat16, shape)
     nb = _sequences(block_table, lengths, new_lens, S)
     _on_current_device(k_new, v_new, cache.k, cache.v, cache.k_scale, cache.v_scale, block_table, lengths, new_lens)
     _check("calib_cache_write", lib().calib_cache_write(
@@ -654,21 +669,24 @@ def sparse_attn_cached(q: torch.Tensor, cache: KVCache, block_table: torch.Tenso
     S, Hq, M, _ = q.shape
     _need(q, "q", torch.bfloat16, (S, Hq, M, D))
     nb = _sequences(block_table, lengths, new_lens, S)
-    if out is None:
-        out = torch.empty((S, Hq, M, D), dtype=out_dtype, device=q.device)
-    if out.dtype not in (torch.bfloat16, torch.float32):
+    if out is not None:
+        out_dtype = out.dtype
+    if out_dtype is not torch.bfloat16 and out_dtype is not torch.float32:
         raise TypeError("out must be bf16 or fp32")
-    _need(out, "out", out.dtype, (S, Hq, M, D))
-    if return_lse and lse is None:
-        lse = torch.empty((S, Hq, M), dtype=torch.float32, device=q.device)
+    if out is None:
+        out = torch.empty_like(q, dtype=out_dtype)
+    else:
+        _need(out, "out", out_dtype, (S, Hq, M, D))
     if lse is not None:
         _need(lse, "lse", torch.float32, (S, Hq, M))
+    elif return_lse:
+        lse = q.new_empty((S, Hq, M), dtype=torch.float32)
     _on_current_device(q, cache.k, cache.v, cache.k_scale, cache.v_scale, block_table, lengths, new_lens, out, lse,
                        None if blist is None else blist.row_ptr)
     need = _workspace_bytes("sparse_attn_cached_workspace", S, Hq, Hkv, M, D, block, nb)
     space = torch.empty(need, dtype=torch.uint8, device=q.device) if need > 0 else None
     cs = None if blist is None else blist.c_struct()
-    flags = (CALIB_ATTN_OUT_F32 if out.dtype == torch.float32 else 0) | (CALIB_ATTN_CAUSAL if causal else 0)
+    flags = (CALIB_ATTN_OUT_F32 if out_dtype is torch.float32 else 0) | (CALIB_ATTN_CAUSAL if causal else 0)
     scale = 1.0 / math.sqrt(D) if scale is None else scale
     _check("sparse_attn_cached", lib().sparse_attn_cached(
         _ptr(q), _ptr(cache.k), _ptr(cache.v), _ptr(cache.k_scale), _ptr(cache.v_scale), _ptr(block_table),
