@@ -28,6 +28,7 @@
 
 namespace {
 
+constexpr int kSms = 148;
 constexpr uint64_t kDefaultTimeoutNs = 4000000000ull;   // bounded device waits: 4 s
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -425,8 +426,6 @@ calib_status bwd_common(const void* q, const void* k, const void* v, const void*
 }
 
 // ---- 8-bit cache -------------------------------------------------------------------
-constexpr int kSms = 148;
-
 // How a call's work is shared (see cached_attn_kernel): rows per unit (8 or 16), units per K/V head, and `flat`:
 // shares per K/V head and row tile, or 0 for a cluster per unit and no second launch.  Clusters where no sequence
 // can be longer than 2048 keys (5 to 8 steps for each of a CTA's warps, about what the cut's merge costs), or
@@ -706,15 +705,18 @@ calib_status calib_transpose_csr(const int32_t* row_ptr, const int16_t* col_idx,
     if (H < 1 || nq < 1 || nk < 1 || nq > 32767 || nk > 32767) return CALIB_ERR_INVALID;
     if (static_cast<long long>(H) * std::max(nq, nk) > (1ll << 31) - 2) return CALIB_ERR_INVALID;
     if (calib_status s = check_device()) return s;
-    // 128 key blocks per CTA while their bits leave room for two CTAs on an SM (up to about 6900 query blocks),
-    // 32 beyond (131 KB at the most query blocks)
-    const int stride = cdiv(nq, 32) | 1;
-    const int cols = calib::kTransMaxCols * stride * 4 <= 110 * 1024 ? calib::kTransMaxCols : 32;
-    const int bytes = cols * stride * 4;
-    if (calib_status s = ensure_smem(reinterpret_cast<const void*>(calib::transpose_csr_kernel), 32 * 1025 * 4)) return s;
-    calib::transpose_csr_kernel<<<H * cdiv(nk, cols), calib::kTransThreads, bytes, as_stream(stream)>>>(
-        row_ptr, col_idx, H, nq, nk, cols, t_row_ptr_out, t_col_idx_out);
-    return launch_status();
+    // CTAs per head: as many as there are SMs for, at most 8 and one per word of 32 rows.  Each asks for more than
+    // half of an SM's shared memory, so that no two share an SM while others idle (40 heads of 591: 39 us with four
+    // each and two on some SMs).  Tiles of at most 1024 columns (a thread each), and of 80 KB.
+    const int words = cdiv(nq, 32);
+    const int cluster = std::max(1, std::min(std::min(kSms / H, calib::kTransMaxCluster), words));
+    const int per = cdiv(words, cluster), stride = per | 1;
+    const int cols = std::min(std::min(nk, calib::kTransThreads), 80 * 1024 / 4 / stride);
+    const int bytes = std::max(116 * 1024, (cols * stride + per * 32) * 4);
+    auto* fn = calib::transpose_csr_kernel;
+    if (calib_status s = ensure_smem(reinterpret_cast<const void*>(fn), 80 * 1024 + 32768 * 4)) return s;
+    return launch_with(fn, H * cluster, calib::kTransThreads, bytes, as_stream(stream), cluster, false, row_ptr, col_idx, nq,
+                       nk, cluster, cols, t_row_ptr_out, t_col_idx_out);
 }
 
 calib_status calib_cache_write(const void* k_new, const void* v_new, void* k_cache, void* v_cache, float* k_scale,

@@ -289,26 +289,6 @@ __device__ __forceinline__ CachedCell cached_cell(const CachedParams& p, int s, 
     return c;
 }
 
-// Clusters: rank and size, a barrier over all their threads (each thread's earlier shared-memory writes are
-// seen after it), and a load from the same address in another CTA's shared memory.
-__device__ __forceinline__ uint32_t cluster_rank() {
-    uint32_t r;
-    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ void cluster_barrier() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-__device__ __forceinline__ float4 cluster_load(uint32_t addr, uint32_t rank) {
-    float4 v;
-    asm volatile("{\n\t.reg .u32 a;\n\tmapa.shared::cluster.u32 a, %4, %5;\n\t"
-                 "ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [a];\n\t}"
-                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                 : "r"(addr), "r"(rank)
-                 : "memory");
-    return v;
-}
-
 // Attention of a few query rows over a sequence's cached keys: the G query heads of a K/V head
 // times M query tokens are the rows, 8 * NT of them per unit (a cell and a tile of its rows).
 //

@@ -50,6 +50,34 @@ __device__ __forceinline__ uint32_t warp_id() { return threadIdx.x >> 5; }
 // A kernel launched to begin while the one before it ends: waits until that one is done and its writes are seen.
 __device__ __forceinline__ void wait_for_previous_launch() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// Clusters: a CTA's rank, a barrier over all their threads (each thread's earlier shared-memory writes are
+// seen after it), and loads from the same address in another CTA's shared memory.
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_barrier() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ float4 cluster_load(uint32_t addr, uint32_t rank) {
+    float4 v;
+    asm volatile("{\n\t.reg .u32 a;\n\tmapa.shared::cluster.u32 a, %4, %5;\n\t"
+                 "ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [a];\n\t}"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr), "r"(rank)
+                 : "memory");
+    return v;
+}
+__device__ __forceinline__ int cluster_load_int(uint32_t addr, uint32_t rank) {
+    int v;
+    asm volatile("{\n\t.reg .u32 a;\n\tmapa.shared::cluster.u32 a, %1, %2;\n\tld.shared::cluster.u32 %0, [a];\n\t}"
+                 : "=r"(v)
+                 : "r"(addr), "r"(rank)
+                 : "memory");
+    return v;
+}
+
 // ------------------------------------------------------------------------------------
 // mbarrier
 // ------------------------------------------------------------------------------------
