@@ -363,7 +363,7 @@ calib_status launch_bwd(const calib::BwdMaps& m, const calib::BwdParams& p, cuda
     if (calib_status s = ensure_smem(reinterpret_cast<const void*>(fn), L::BYTES)) return s;
     calib::bwd_prepare_kernel<D><<<static_cast<int>((threads + 255) / 256), 256, 0, st>>>(p, rows);
     if (calib_status s = launch_status()) return s;
-    return launch_with(fn, p.geo.H * (p.geo.nk + p.geo.nq), calib::kBwdThreads, L::BYTES, st, 1, true, m, p);
+    return launch_with(fn, p.geo.H * (p.geo.nk + p.geo.nq), calib::bwd_threads(BLK), L::BYTES, st, 1, true, m, p);
 }
 
 calib_status bwd_common(const void* q, const void* k, const void* v, const void* o, const void* dout,

@@ -112,19 +112,22 @@ __global__ void __launch_bounds__(256) bwd_prepare_kernel(const BwdParams p, int
     }
 }
 
-constexpr int kBwdThreads = 320;          // warp 0 TMA, warp 1 MMA, warps 2..9 arithmetic
-constexpr int kBwdArith = 256;
+// Arithmetic warps, four for each part of a tile's columns (one per 32 TMEM lanes).
+constexpr int kBwdParts = 4;
+constexpr int bwd_parts(int blk) { return blk == 128 ? kBwdParts : 2; }
+constexpr int bwd_threads(int blk) { return 64 + 128 * bwd_parts(blk); }   // warp 0 TMA, warp 1 MMA
 
 // Tensor-memory columns: S and dP (fp32, BLK columns each), P and dS (bf16 pairs, BLK / 2 each), the
 // accumulators (D each) and, for dQ, Q and dO (bf16 pairs, D / 2 each).  All of it fits 512 columns except
-// at D = BLK = 128; there P overwrites S and dS overwrites dP, each half-row's columns by the warp that
-// loaded them, and the next S (dP) waits for the product that reads P (dS).  HALF: columns between the two
-// halves of P or dS.
+// at D = BLK = 128; there P overwrites S and dS overwrites dP, each part's columns by the warp that
+// loaded them, and the next S (dP) waits for the product that reads P (dS).  STEP: columns between two
+// parts of P or dS.
 template <int D, int BLK>
 struct BwdTmem {
     static constexpr bool SEP = 3 * BLK + 2 * D <= 512;
     static constexpr uint32_t S = 0, DP = BLK;
-    static constexpr uint32_t P = SEP ? 2 * BLK : S, HALF = SEP ? BLK / 4 : BLK / 2;
+    static constexpr int NP = bwd_parts(BLK), HC = BLK / NP;   // parts of a tile's columns, columns each
+    static constexpr uint32_t P = SEP ? 2 * BLK : S, STEP = SEP ? HC / 2 : HC;
     static constexpr uint32_t DS = SEP ? 2 * BLK + BLK / 2 : DP;
     static constexpr uint32_t ACC = SEP ? 3 * BLK : 2 * BLK;
     static constexpr uint32_t Q = ACC + D, DO = Q + D / 2;
@@ -241,12 +244,12 @@ struct BwdSmem {
 //   warp 0     TMA: K, V once; Q (with its LSE and delta) and dO tiles through two rings.
 //   warp 1     MMA issuer: S, dP of tile 0; then per tile the next S, dV, the next dP, dK (dV, the next S, dK, the
 //              next dP where P and dS share columns with S and dP).
-//   warps 2..9 arithmetic, two warps per 32 keys, half of a tile's queries each.
+//   the others arithmetic: two or four warps per 32 keys, a part of a tile's queries each.
 template <int D, int BLK, int ST>
 __device__ __forceinline__ void bwd_kv(const BwdMaps& m, const BwdParams& p, int id) {
     using L = BwdSmem<D, BLK, ST>;
     using T = BwdTmem<D, BLK>;
-    constexpr int CH = L::CH, HC = BLK / 2;
+    constexpr int CH = L::CH, HC = T::HC;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     const uint32_t sbase = smem_u32(smem);
@@ -273,11 +276,11 @@ __device__ __forceinline__ void bwd_kv(const BwdMaps& m, const BwdParams& p, int
             mbar_init(bar(L::B_BE + s), 1);
         }
         mbar_init(bar(L::B_SF), 1);
-        mbar_init(bar(L::B_SE), kBwdArith);
+        mbar_init(bar(L::B_SE), 128 * T::NP);
         mbar_init(bar(L::B_DPF), 1);
-        mbar_init(bar(L::B_DPE), kBwdArith);
-        mbar_init(bar(L::B_PF), kBwdArith);
-        mbar_init(bar(L::B_DSF), kBwdArith);
+        mbar_init(bar(L::B_DPE), 128 * T::NP);
+        mbar_init(bar(L::B_PF), 128 * T::NP);
+        mbar_init(bar(L::B_DSF), 128 * T::NP);
         mbar_init(bar(L::B_END), 1);
         mbar_init(bar(L::B_DRAIN), 1);
         *abort_flag = 0;
@@ -352,12 +355,12 @@ __device__ __forceinline__ void bwd_kv(const BwdMaps& m, const BwdParams& p, int
         // acc[keys x D] += src[keys x queries] (bf16 in TMEM) x ring tile
         auto grads = [&](uint32_t acc, uint32_t src, uint32_t off_t, int s, bool first) {
 #pragma unroll
-            for (int hf = 0; hf < 2; ++hf)
+            for (int hf = 0; hf < T::NP; ++hf)
 #pragma unroll
                 for (int kk = 0; kk < HC / 16; ++kk) {
                     const uint64_t bd =
                         smem_desc_sw128(sbase + off_t + s * L::T_BYTES + (hf * HC + kk * 16) * 128, L::CHUNK, 1024);
-                    umma_ts(tmem + acc, tmem + src + hf * T::HALF + kk * 8, bd, idesc_g, (!first || hf > 0 || kk > 0) ? 1u : 0u);
+                    umma_ts(tmem + acc, tmem + src + hf * T::STEP + kk * 8, bd, idesc_g, (!first || hf > 0 || kk > 0) ? 1u : 0u);
                 }
         };
         bool ok = mbar_wait_warp(bar(L::B_R), 0, ctl);
@@ -428,7 +431,7 @@ __device__ __forceinline__ void bwd_kv(const BwdMaps& m, const BwdParams& p, int
         if (ok && elect_one()) umma_commit(bar(L::B_END));
     } else if (warp >= 2) {
         // ===================== arithmetic and output ====================================
-        const int hf = static_cast<int>(warp - 2) >> 2;    // half of every tile's queries
+        const int hf = static_cast<int>(warp - 2) >> 2;    // part of every tile's queries
         const uint32_t q4 = warp & 3;
         const int r = static_cast<int>(q4 * 32 + lane);    // key of the block == TMEM lane
         const uint32_t lane_base = (q4 * 32) << 16;
@@ -464,7 +467,7 @@ __device__ __forceinline__ void bwd_kv(const BwdMaps& m, const BwdParams& p, int
             }
             // the previous P has been read by its product
             if (T::SEP && t > 0 && !(ok = mbar_wait_warp(bar(L::B_BE + (t - 1) % ST), ((t - 1) / ST) & 1, ctl))) break;
-            tmem_put<HC>(tmem + lane_base + T::P + hf * T::HALF, pk);
+            tmem_put<HC>(tmem + lane_base + T::P + hf * T::STEP, pk);
             tmem_wait_st();
             tc_fence_before();
             mbar_arrive(bar(L::B_PF));
@@ -491,7 +494,7 @@ __device__ __forceinline__ void bwd_kv(const BwdMaps& m, const BwdParams& p, int
             }
             // the previous dS has been read by its product
             if (T::SEP && t > 0 && !(ok = mbar_wait_warp(bar(L::B_AE + (t - 1) % ST), ((t - 1) / ST) & 1, ctl))) break;
-            tmem_put<HC>(tmem + lane_base + T::DS + hf * T::HALF, pk);
+            tmem_put<HC>(tmem + lane_base + T::DS + hf * T::STEP, pk);
             tmem_wait_st();
             tc_fence_before();
             mbar_arrive(bar(L::B_DSF));
@@ -499,14 +502,13 @@ __device__ __forceinline__ void bwd_kv(const BwdMaps& m, const BwdParams& p, int
         if (ok && n > 0) ok = mbar_wait_warp(bar(L::B_END), 0, ctl);
         if (ok) {
             tc_fence_after();
-            // warps 2..5 write dV, warps 6..9 dK
+            // 32 columns at a time: the parts' warps in turn, dV's columns first, then dK's
             const int tok = j * BLK + r;
             const bool write = r < BLK && tok < g.N;
             const size_t at = (static_cast<size_t>(h) * g.N + tok) * D;
-#pragma unroll
-            for (int c = 0; c < D; c += 32)
-                put_grad32(hf ? p.dk : p.dv, at + c, p.grad_f32, tmem + lane_base + T::ACC + hf * D + c,
-                           hf ? p.scale : 1.f, n > 0, write);
+            for (int c = hf * 32; c < 2 * D; c += T::NP * 32)
+                put_grad32(c < D ? p.dv : p.dk, at + c % D, p.grad_f32, tmem + lane_base + T::ACC + c, c < D ? 1.f : p.scale,
+                           n > 0, write);
         }
     }
 
@@ -542,7 +544,7 @@ template <int D, int BLK, int ST>
 __device__ __forceinline__ void bwd_q(const BwdMaps& m, const BwdParams& p, int id) {
     using L = BwdSmem<D, BLK, ST>;
     using T = BwdTmem<D, BLK>;
-    constexpr int CH = L::CH, HC = BLK / 2;
+    constexpr int CH = L::CH, HC = T::HC;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     const uint32_t sbase = smem_u32(smem);
@@ -574,10 +576,10 @@ __device__ __forceinline__ void bwd_q(const BwdMaps& m, const BwdParams& p, int 
             mbar_init(bar(L::B_BE + s), 1);
         }
         mbar_init(bar(L::B_SF), 1);
-        mbar_init(bar(L::B_SE), kBwdArith);
+        mbar_init(bar(L::B_SE), 128 * T::NP);
         mbar_init(bar(L::B_DPF), 1);
-        mbar_init(bar(L::B_DPE), kBwdArith);
-        mbar_init(bar(L::B_DSF), kBwdArith);
+        mbar_init(bar(L::B_DPE), 128 * T::NP);
+        mbar_init(bar(L::B_DSF), 128 * T::NP);
         mbar_init(bar(L::B_END), 1);
         mbar_init(bar(L::B_DRAIN), 1);
         *abort_flag = 0;
@@ -704,12 +706,12 @@ __device__ __forceinline__ void bwd_q(const BwdMaps& m, const BwdParams& p, int 
             tc_fence_after();
             if (elect_one()) {
 #pragma unroll
-                for (int hf = 0; hf < 2; ++hf)
+                for (int hf = 0; hf < T::NP; ++hf)
 #pragma unroll
                     for (int kk = 0; kk < HC / 16; ++kk) {
                         const uint64_t bd = smem_desc_sw128(
                             sbase + L::OFF_A + s * L::T_BYTES + (hf * HC + kk * 16) * 128, L::CHUNK, 1024);
-                        umma_ts(tmem + T::ACC, tmem + T::DS + hf * T::HALF + kk * 8, bd, idesc_g,
+                        umma_ts(tmem + T::ACC, tmem + T::DS + hf * T::STEP + kk * 8, bd, idesc_g,
                                 (t > 0 || hf > 0 || kk > 0) ? 1u : 0u);
                     }
                 umma_commit(bar(L::B_AE + s));             // K's stage, and dS's columns, are free
@@ -719,7 +721,7 @@ __device__ __forceinline__ void bwd_q(const BwdMaps& m, const BwdParams& p, int 
         if (ok && elect_one()) umma_commit(bar(L::B_END));
     } else if (warp >= 2) {
         // ===================== arithmetic and output ====================================
-        const int hf = static_cast<int>(warp - 2) >> 2;    // half of every tile's keys
+        const int hf = static_cast<int>(warp - 2) >> 2;    // part of every tile's keys
         const uint32_t q4 = warp & 3;
         const int r = static_cast<int>(q4 * 32 + lane);    // query of the block == TMEM lane
         const uint32_t lane_base = (q4 * 32) << 16;
@@ -771,7 +773,7 @@ __device__ __forceinline__ void bwd_q(const BwdMaps& m, const BwdParams& p, int 
             }
             // the previous dS has been read by its product
             if (T::SEP && t > 0 && !(ok = mbar_wait_warp(bar(L::B_AE + (t - 1) % ST), ((t - 1) / ST) & 1, ctl))) break;
-            tmem_put<HC>(tmem + lane_base + T::DS + hf * T::HALF, pk);
+            tmem_put<HC>(tmem + lane_base + T::DS + hf * T::STEP, pk);
             tmem_wait_st();
             tc_fence_before();
             mbar_arrive(bar(L::B_DSF));
@@ -782,8 +784,7 @@ __device__ __forceinline__ void bwd_q(const BwdMaps& m, const BwdParams& p, int 
             const int tok = rep && row_ok ? anchor_token(g, qrow) : qrow;
             const int copies = rep && row_ok ? anchor_copies(g, qrow) : 1;
             const size_t at = (static_cast<size_t>(h) * g.N + tok) * D;
-#pragma unroll
-            for (int c = hf * (D / 2); c < (hf + 1) * (D / 2); c += 32) {
+            for (int c = hf * 32; c < D; c += T::NP * 32) {
                 put_grad32(p.dq, at + c, p.grad_f32, tmem + lane_base + T::ACC + c, p.scale, n > 0, row_ok);
                 // the tokens that only take an anchor's output are no queries of a repeat head
                 for (int y = 1; y < copies; ++y)
@@ -817,7 +818,7 @@ __device__ __forceinline__ void bwd_q(const BwdMaps& m, const BwdParams& p, int 
 // Both gradients in one launch: the key blocks' items first (four products a tile), then the query blocks'
 // (three), which fill the SMs that run out of the former.
 template <int D, int BLK, int ST>
-__global__ void __launch_bounds__(kBwdThreads, 1) bwd_kernel(const __grid_constant__ BwdMaps m, const __grid_constant__ BwdParams p) {
+__global__ void __launch_bounds__(bwd_threads(BLK), 1) bwd_kernel(const __grid_constant__ BwdMaps m, const __grid_constant__ BwdParams p) {
     const int n_kv = p.geo.H * p.geo.nk;
     const int id = static_cast<int>(blockIdx.x);
     if (id < n_kv) bwd_kv<D, BLK, ST>(m, p, id);
