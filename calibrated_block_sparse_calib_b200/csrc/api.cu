@@ -36,12 +36,18 @@ int cdiv(long long a, long long b) { return static_cast<int>((a + b - 1) / b); }
 
 cudaStream_t as_stream(void* s) { return reinterpret_cast<cudaStream_t>(s); }
 
-// sm_100 check, cached per device.
+// sm_100 check, cached per device.  A thread that has made no CUDA call yet (autograd's, on its first backward pass) has
+// no context, which the driver's tensor-map encoder needs: setting the device it is on anyway gives it one.
 calib_status check_device() {
     static std::mutex mu;
     static std::set<int> ok_devices;
+    static thread_local int bound = -1;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return CALIB_ERR_CUDA;
+    if (bound != dev) {
+        if (cudaSetDevice(dev) != cudaSuccess) return CALIB_ERR_CUDA;
+        bound = dev;
+    }
     std::lock_guard<std::mutex> lk(mu);
     if (ok_devices.count(dev)) return CALIB_OK;
     int major = 0;
@@ -430,8 +436,9 @@ calib_status bwd_common(const void* q, const void* k, const void* v, const void*
 // shares per K/V head and row tile, or 0 for a cluster per unit and no second launch.  Clusters where no sequence
 // can be longer than 2048 keys (5 to 8 steps for each of a CTA's warps, about what the cut's merge costs), or
 // 8192 if the GPU has room for clusters of 8, or where the units fill the GPU 8 times and more; a cluster has one step
-// for each of its warps, as far as 8 CTAs and the GPU's places go.  The shares fill the GPU's places once, or twice
-// where once would leave more than a tenth of them empty.
+// for each of its warps, as far as 8 CTAs and the GPU's places go.  The number of shares is the one that takes the
+// fewest steps in all if every sequence is as long as the table allows: rounds of CTAs times a share's steps and 6
+// more for its start and end.
 struct CachedPlan {
     int nt, tiles, flat, cluster;
     long long units, grid;
@@ -454,10 +461,17 @@ CachedPlan cached_plan(int S, int Hq, int Hkv, int M, int D, int B, int nb) {
         while (c.cluster < 8 && c.cluster * warps < keys / calib::kChunk && c.units * c.cluster * 2 <= places) c.cluster *= 2;
         c.grid = c.units * c.cluster;
     } else {
-        long long shares = std::max(1ll, places / columns);
-        if (shares * columns * 10 < places * 9) shares = std::max(1ll, 2 * places / columns);
-        const long long total = S * (keys / calib::kChunk + calib::kUnitCost);
-        c.flat = static_cast<int>(std::min(shares, std::max(1ll, total / calib::kMinShare)));
+        const long long total = S * (keys / calib::kChunk + calib::kUnitCost), warps = D == 128 && c.nt == 1 ? 12 : 8;
+        double best = 0.;
+        for (long long shares = 1; shares <= std::max(1ll, 3 * places / columns) && shares <= std::max(1ll, total / calib::kMinShare);
+             ++shares) {
+            const double cost = static_cast<double>(cdiv(shares * columns, places)) *
+                                (static_cast<double>(total) / static_cast<double>(shares * warps) + 6.);
+            if (c.flat == 0 || cost < best) {
+                c.flat = static_cast<int>(shares);
+                best = cost;
+            }
+        }
         c.grid = c.flat * columns;
         const int64_t slots = 2 * c.grid * 8 * c.nt;
         c.part_o = (c.units * 8 + 15) / 16 * 16;

@@ -182,8 +182,9 @@ constexpr int kMinShare = 64;             // no CTA gets less than this (a unit'
 constexpr float kPShift = 15.f;           // P is held as 2^(x - m + 15) <= 2^15
 
 // Warps per CTA and CTAs per SM: a chunk is a chain of shared memory reads, conversions, two products and a
-// softmax, and with two warps a scheduler their latencies, not the memory, set the pace (8 warps per SM at
-// D = 128: 5.4 TB/s, 12: see below); more rows (NT = 2) leave registers for 8 (16 at D = 64).
+// softmax, whose latencies the other warps of a scheduler hide: 12 warps per SM at D = 128 (4 x 131072 tokens, 8
+// heads: 170 us; with 8 warps and a ring of three, 167 to 186 us from run to run), 16 at D = 64.  More rows
+// (NT = 2) leave registers for 8 at D = 128.
 template <int D, int NT>
 struct CachedSmem {
     static constexpr int RW = 8 * NT;                                  // query rows

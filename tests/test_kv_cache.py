@@ -447,3 +447,62 @@ def test_refusals_on_the_gpu():
         ops.sparse_attn_cached(torch.zeros(S, 3, 1, D, dtype=torch.bfloat16, device="cuda"), cache, table, n)
     with pytest.raises(ValueError, match="shape"):
         ops.cache_write(cache, q[:, :1].contiguous(), q, table, n)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("D", [64, 128])
+def test_a_live_nan_is_not_hidden(D):
+    """NaN in a value (at every place of a word, each of which is converted in its own way) or in a key of a live
+    token shows in the outputs that weigh it, and not in other heads or sequences."""
+    S, H, B = 2, 2, 64
+    cache, table = _cache(np.random.default_rng(11), S, H, D, B, 2)
+    q = torch.randn(S, H, 1, D, generator=torch.Generator().manual_seed(11)).to(torch.bfloat16).cuda()
+    clean = ops.sparse_attn_cached(q, cache, table, _ints([100, 90]))
+    page = int(table[0, 1])
+    for d in range(8):
+        for byte in (0x7F, 0xFF):
+            bad = ops.KVCache(cache.k, cache.v.view(torch.uint8).clone().view(torch.float8_e4m3fn), cache.k_scale, cache.v_scale)
+            bad.v.view(torch.uint8)[page, 1, 13, d] = byte
+            o = ops.sparse_attn_cached(q, bad, table, _ints([100, 90]))
+            assert torch.isnan(o[0, 1, 0, d]) and torch.equal(o[0, 0], clean[0, 0]) and torch.equal(o[1], clean[1])
+            bad = ops.KVCache(cache.k.view(torch.uint8).clone().view(torch.float8_e4m3fn), cache.v, cache.k_scale, cache.v_scale)
+            bad.k.view(torch.uint8)[page, 1, 13, d] = byte
+            o, lse = ops.sparse_attn_cached(q, bad, table, _ints([100, 90]), return_lse=True)
+            assert torch.isnan(o[0, 1]).all() and torch.isnan(lse[0, 1]).all() and torch.equal(o[1], clean[1])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("S,Hq,Hkv,M,D,B,longest", [
+    (40, 160, 160, 1, 128, 64, 100),      # 6400 units: more than eight rounds, a CTA each
+    (7, 160, 160, 1, 128, 64, 2200),      # more heads than places, lines of seven sequences
+    (300, 2, 2, 1, 64, 64, 2300),         # long lines of short sequences: many units a share
+    (2, 1, 1, 1, 128, 128, 9000),         # two sequences, one head: every share of one line
+    (1, 4, 4, 1, 64, 128, 8192),          # clusters of 8
+    (3, 8, 4, 30, 128, 128, 2500)])       # several row tiles, cut
+def test_every_way_of_sharing_the_work(S, Hq, Hkv, M, D, B, longest):
+    """Ragged lengths from 0 up under a table for the longest, so that cuts fall everywhere: against each sequence
+    alone in a call of its own (whose cuts are others), which the cases above hold to the oracle."""
+    rng = np.random.default_rng(S + longest)
+    nb = ops.nblocks(longest, B)
+    cache, table = _cache(rng, S, Hkv, D, B, nb)
+    lengths = np.minimum(longest, (rng.random(S) ** 3 * 1.2 * longest).astype(np.int32))
+    lengths[0] = longest
+    if S > 1:
+        lengths[-1] = 0
+    new = np.minimum(lengths, rng.integers(1, M + 1, S)).astype(np.int32)
+    q = torch.randn(S, Hq, M, D, generator=torch.Generator().manual_seed(12)).to(torch.bfloat16).cuda()
+    o, lse = ops.sparse_attn_cached(q, cache, table, _ints(lengths.tolist()), new_lens=_ints(new.tolist()), return_lse=True,
+                                    out_dtype=torch.float32)
+    ops.device_check()
+    for s in ({0, 1, S // 2, S - 1} & set(range(S))):
+        n = max(1, int(lengths[s]))
+        one, l1 = ops.sparse_attn_cached(q[s:s + 1].contiguous(), cache, table[s:s + 1, :ops.nblocks(n, B)].contiguous(),
+                                         _ints([int(lengths[s])]), new_lens=_ints([int(new[s])]), return_lse=True,
+                                         out_dtype=torch.float32)
+        # the same weights in another order of sums: 2 L 2^-24 of sum P |v|, and the roundings of P at another maximum
+        # (2^-11 each way, at most)
+        most = 448 * float(cache.v_scale.max())
+        assert float((o[s] - one[0]).abs().max()) <= (2 * 2.0 ** -11 + 2 * n * U32) * most
+        fin = torch.isfinite(l1[0])
+        assert torch.equal(torch.isfinite(lse[s]), fin)
+        assert float((lse[s] - l1[0])[fin].abs().max().nan_to_num(0) if fin.any() else 0) <= 2 * n * U32 + 2.0 ** -18
