@@ -399,13 +399,13 @@ class BlockList:
     work: Optional[torch.Tensor] = None
 
     def c_struct(self) -> _BlockListC:
-        _need(self.row_ptr, "row_ptr", torch.int32, (self.H * self.nq + 1,))
-        _need(self.col_idx, "col_idx", torch.int16)
-        if self.work is not None:
-            _need(self.work, "work", torch.int32)
-        return _BlockListC(self.H, self.nq, self.nk, self.block, self.row_ptr.data_ptr(),
-                           self.col_idx.data_ptr(), 0 if self.work is None else self.work.data_ptr(),
-                           0 if self.work is None else self.work.numel())
+        rp, ci, work = self.row_ptr, self.col_idx, self.work
+        _need(rp, "row_ptr", torch.int32, (self.H * self.nq + 1,))
+        _need(ci, "col_idx", torch.int16)
+        if work is None:
+            return _BlockListC(self.H, self.nq, self.nk, self.block, rp.data_ptr(), ci.data_ptr(), 0, 0)
+        _need(work, "work", torch.int32)
+        return _BlockListC(self.H, self.nq, self.nk, self.block, rp.data_ptr(), ci.data_ptr(), work.data_ptr(), work.numel())
 
     def validate(self) -> "BlockList":
         """Copy the list back to the host and check its structure (rows within col_idx,
@@ -494,16 +494,17 @@ def sparse_attn_fwd_repeat(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, bl
 
 def _bwd(name, q, k, v, out, dout, lse, blist, blist_t, scale, grads, grad_dtype, n_anchor, geometry):
     H, N, D = shape = q.shape
-    _need(q, "q", torch.bfloat16)
-    _need(k, "k", torch.bfloat16, shape)
-    _need(v, "v", torch.bfloat16, shape)
+    bf16 = torch.bfloat16
+    _need(q, "q", bf16)
+    _need(k, "k", bf16, shape)
+    _need(v, "v", bf16, shape)
     io = out.dtype
-    if io is not torch.bfloat16 and io is not torch.float32:
+    if io is not bf16 and io is not torch.float32:
         raise TypeError("out must be bf16 or fp32")
     _need(out, "out", io, shape)
     _need(dout, "dout", io, shape)
     _need(lse, "lse", torch.float32, (H, N))
-    if grad_dtype is not torch.bfloat16 and grad_dtype is not torch.float32:
+    if grad_dtype is not bf16 and grad_dtype is not torch.float32:
         raise TypeError("gradients are bf16 or fp32")
     dq, dk, dv = grads
     if dq is None:
@@ -524,13 +525,14 @@ def _bwd(name, q, k, v, out, dout, lse, blist, blist_t, scale, grads, grad_dtype
     flags = (CALIB_ATTN_OUT_F32 if io is torch.float32 else 0) | \
         (CALIB_ATTN_GRAD_F32 if grad_dtype is torch.float32 else 0)
     need = _workspace_bytes("sparse_attn_bwd_workspace", H, N, D, blist.block, n_anchor, flags)
-    space = torch.empty(max(1, need), dtype=torch.uint8, device=q.device)
+    space = q.new_empty(max(1, need), dtype=torch.uint8)
     cs, ct = blist.c_struct(), blist_t.c_struct()
     sizes = (H, N, D) if geometry is None else (H, D, *geometry)
     scale = 1.0 / math.sqrt(D) if scale is None else scale
     _check(name, getattr(lib(), name)(
-        _ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(dout), _ptr(lse), _ptr(dq), _ptr(dk), _ptr(dv), *sizes, scale,
-        ctypes.byref(cs), ctypes.byref(ct), flags, _ptr(space), space.numel(), _stream()))
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), dout.data_ptr(), lse.data_ptr(), dq.data_ptr(),
+        dk.data_ptr(), dv.data_ptr(), *sizes, scale, ctypes.byref(cs), ctypes.byref(ct), flags, space.data_ptr(), need,
+        _stream()))
     return dq, dk, dv
 
 
@@ -684,7 +686,7 @@ def sparse_attn_cached(q: torch.Tensor, cache: KVCache, block_table: torch.Tenso
     _on_current_device(q, cache.k, cache.v, cache.k_scale, cache.v_scale, block_table, lengths, new_lens, out, lse,
                        None if blist is None else blist.row_ptr)
     need = _workspace_bytes("sparse_attn_cached_workspace", S, Hq, Hkv, M, D, block, nb)
-    space = torch.empty(need, dtype=torch.uint8, device=q.device) if need > 0 else None
+    space = q.new_empty(need, dtype=torch.uint8) if need > 0 else None
     cs = None if blist is None else blist.c_struct()
     flags = (CALIB_ATTN_OUT_F32 if out_dtype is torch.float32 else 0) | (CALIB_ATTN_CAUSAL if causal else 0)
     scale = 1.0 / math.sqrt(D) if scale is None else scale
