@@ -231,8 +231,7 @@ __device__ __forceinline__ uint2 lds64(uint32_t a) {
 // Byte b of x and byte b of y, both e4m3, as a half-precision pair 2^-8 times as large, exactly: the byte's
 // sign, exponent and mantissa fields are half precision's top ones with the exponent's first bit left out,
 // so 7 places up and that bit (filled by the sign) cleared is the number over 2^8, subnormal ones too.
-// Three integer instructions where the conversion instruction is one on the slower XU pipe.  NaN comes
-// out as 480 / 2^8.
+// Three integer instructions; NaN comes out as 480 / 2^8.
 template <int b>
 __device__ __forceinline__ uint32_t e4m3_pair_shifted(uint32_t x, uint32_t y) {
     constexpr uint32_t sel = b | (8 + b) << 4 | (4 + b) << 8 | (12 + b) << 12;   // byte, its sign eight times; twice
@@ -311,9 +310,10 @@ __device__ __forceinline__ CachedCell cached_cell(const CachedParams& p, int s, 
 // O^T = V^T P^T as 16x8x16 MMAs, which wastes nothing at 8 rows where rows as M would fill half of a
 // tile.  (A tcgen05 tile has 128 rows in M; with keys there it would need the 8-bit operands
 // rewritten as 16-bit ones in shared memory first.)
-//   - e4m3 is exact in half precision: K and half of V by the conversion instruction, the
-//     other half of V by integer ones (all of them on the XU pipe, 16 lanes a clock, kept that busy to
-//     100%); the NaNs of that half are looked for apart, and make their chunk's product NaN.  Q is scaled by a power of two per row so that its largest
+//   - e4m3 is exact in half precision: by the conversion instruction, except half of V at D = 128, where integer
+//     instructions share the work (4 x 131072 tokens: 178 us without that, 171 with; at D = 64, 34 without
+//     and 37 with, on 8 x 32760 tokens at 30%).  The NaNs of that half are looked for apart, and make their chunk's
+//     product NaN.  Q is scaled by a power of two per row so that its largest
 //     value is in [2^14, 2^15): bf16's 8 bits fit half's 11, and values down to 2^-30 of the
 //     largest stay exact.  P is kept as 2^(x - m + 15), so that half precision holds weights down
 //     to 2^-39 of the largest; its rounding (2^-11 relative at most) is to nearest, without bias.
@@ -330,6 +330,7 @@ __global__ void __launch_bounds__((CachedSmem<D, NT>::THREADS), (CachedSmem<D, N
 cached_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                    const __grid_constant__ CachedParams p) {
     using L = CachedSmem<D, NT>;
+    constexpr bool kShifted = D == 128;                     // half of V converted by integer instructions
     constexpr int ST = L::STAGES, KS = D / 16, MT = D / 16, RW = L::RW, CPB = B / kChunk, W = L::WARPS;
     extern __shared__ uint8_t smem_raw[];
     __shared__ long long scan_sum[W];
@@ -689,10 +690,21 @@ cached_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                 }
 #pragma unroll
                 for (int e = 0; e < D / 32; ++e) {
-                    nan |= e4m3_nan_bits(u[0][e]) | e4m3_nan_bits(u[1][e]);
-                    nan |= e4m3_nan_bits(u[2][e]) | e4m3_nan_bits(u[3][e]);
-                    const uint32_t a0 = e4m3_pair_shifted<0>(u[0][e], u[1][e]), a1 = e4m3_pair_shifted<1>(u[0][e], u[1][e]);
-                    const uint32_t a2 = e4m3_pair_shifted<0>(u[2][e], u[3][e]), a3 = e4m3_pair_shifted<1>(u[2][e], u[3][e]);
+                    uint32_t a0, a1, a2, a3;
+                    if constexpr (kShifted) {
+                        nan |= e4m3_nan_bits(u[0][e]) | e4m3_nan_bits(u[1][e]);
+                        nan |= e4m3_nan_bits(u[2][e]) | e4m3_nan_bits(u[3][e]);
+                        a0 = e4m3_pair_shifted<0>(u[0][e], u[1][e]);
+                        a1 = e4m3_pair_shifted<1>(u[0][e], u[1][e]);
+                        a2 = e4m3_pair_shifted<0>(u[2][e], u[3][e]);
+                        a3 = e4m3_pair_shifted<1>(u[2][e], u[3][e]);
+                    } else {
+                        const uint32_t y0 = __byte_perm(u[0][e], u[1][e], 0x5140), y1 = __byte_perm(u[2][e], u[3][e], 0x5140);
+                        a0 = e4m3x2_to_f16x2(y0);
+                        a1 = e4m3x2_hi_to_f16x2(y0);
+                        a2 = e4m3x2_to_f16x2(y1);
+                        a3 = e4m3x2_hi_to_f16x2(y1);
+                    }
                     const uint32_t x0 = __byte_perm(u[0][e], u[1][e], 0x7362), x1 = __byte_perm(u[2][e], u[3][e], 0x7362);
                     const uint32_t b0 = e4m3x2_to_f16x2(x0), b1 = e4m3x2_hi_to_f16x2(x0);
                     const uint32_t b2 = e4m3x2_to_f16x2(x1), b3 = e4m3x2_hi_to_f16x2(x1);
@@ -703,9 +715,10 @@ cached_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                     }
                 }
             }
-            // even tiles hold values over 2^8 (bytes 0 and 1), odd ones the values themselves; O is kept over 2^8
-            const float vs_mt[2] = {__any_sync(0xffffffffu, (nan & 0x8080u) != 0u) ? __int_as_float(0x7FC00000) : vs,
-                                    vs * 0.00390625f};
+            // even tiles (bytes 0 and 1) hold values over 2^8 where they were shifted, odd ones the values themselves; O is
+            // kept over 2^8
+            float vs_mt[2] = {vs * 0.00390625f, vs * 0.00390625f};
+            if constexpr (kShifted) vs_mt[0] = __any_sync(0xffffffffu, (nan & 0x8080u) != 0u) ? __int_as_float(0x7FC00000) : vs;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
