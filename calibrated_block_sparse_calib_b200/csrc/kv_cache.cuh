@@ -56,7 +56,8 @@ constexpr int kWriteThreads = 256;
 // then rounded again at the new one (a second rounding, up to half an e4m3 step); if it does not
 // grow their bytes stay.  So the largest value of a block is never cut off, and one token costs one
 // row, not its block.  Bytes at and behind the sequence's end are left as they were.
-// Bound by memory: 2 bytes in and 1 out per value.
+// Bound by memory: 2 bytes in and 1 out per value (8 prompts of up to 4096 tokens, 8 heads, 101 MB: 22.6 us,
+// 4.5 TB/s).  A CTA per block and head, so that the largest magnitude needs one barrier and the tokens one load.
 template <int D, int B>
 __global__ void __launch_bounds__(kWriteThreads) cache_write_kernel(const CacheWriteParams p) {
     constexpr int CPR = D / 8;                             // 8-value chunks per token
@@ -177,7 +178,9 @@ struct CachedParams {
 };
 
 constexpr int kChunk = 32;                // keys per warp and step
-constexpr int kUnitCost = 16;             // a unit's own cost (Q, merge, output) in chunks
+// A unit's own cost (Q, merge, output) in chunks: 4, 16 and 32 measured 67.4, 65.6 and 64.7 us on 32 ragged sequences
+// of 8192 tokens at most, 36.6, 37.2 and 37.6 us on 8 of 32760 at 30%.
+constexpr int kUnitCost = 16;
 constexpr int kMinShare = 64;             // no CTA gets less than this (a unit's own cost included)
 constexpr float kPShift = 15.f;           // P is held as 2^(x - m + 15) <= 2^15
 

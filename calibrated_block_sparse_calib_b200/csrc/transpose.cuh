@@ -16,8 +16,8 @@
 // every run.
 // What bounds it is instructions, most of them in the writing (a column has few words per CTA);
 // the 14 MB that a 40 x 591 x 591 list at 25% reads and writes would take 2.2 us of HBM time.
-// Measured there: 46 us with a bisection per row and 32 columns, 39 us with every row read by the
-// CTAs of each 128 columns, and as it is: see the tables.
+// Measured there: 46 us with a bisection per row and 32 columns a CTA, 39 us with every row read by the
+// CTAs of each 128 columns, 29 us as it is; 6 us at 12 x 64 x 64 (graph replays).
 #pragma once
 #include "ptx.cuh"
 #include "select.cuh"
