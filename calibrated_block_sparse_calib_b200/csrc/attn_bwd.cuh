@@ -13,8 +13,7 @@
 // products' work, 1250 of all seven's): the products run at about 100 cycles per 128 x 128 x 16 where 64 is the
 // nominal rate, S and dP of the key blocks' side slower than the others because both their operands come from
 // shared memory (tensor memory is full).  Over seconds the power cap sets the time, 2.4 ms.
-// P, dS and (repeat heads, fp32 output) dO enter the products as bf16, rounded to nearest: 2^-9 relative at random
-// signs, which leaves gradients 0.003 (relative 2-norm) from the 64-bit result where rounding only the results
+// P, dS and (repeat heads, fp32 output) dO enter the products as bf16, rounded to nearest, which leaves gradients 0.003 (relative 2-norm) from the 64-bit result where rounding only the results
 // leaves 0.0017.
 // Tried and dropped (4 x 32760 x 128 unless said): dV and dK before the next S: +13%; one exponential pair in two or
 // four on the FMA pipe: +-1%; one arrival per warp instead of per thread on the arithmetic's barriers: +-1%; a
@@ -62,7 +61,7 @@ __device__ __forceinline__ int anchor_copies(const AttnParams& p, int a) {
 // row, and the operands that the products need as bf16: dO when it came as fp32, and for a repeat head the
 // anchors' rows of Q with dO and delta summed over the tokens that take the anchor's output (its O
 // and LSE are the same in all of them).  The sum is fp32 and dO enters the products as bf16, so it
-// is rounded once (2^-9 relative), as P and dS are.  Rows past the sequence get -LSE = -inf, which
+// is rounded once (2^-8 relative at most), as P and dS are.  Rows past the sequence get -LSE = -inf, which
 // makes their probabilities 0; so do rows with nothing kept.
 // Reads dO and O once: 2 x 268 MB at 12 x 32760 x 128, bound by memory.
 template <int D>

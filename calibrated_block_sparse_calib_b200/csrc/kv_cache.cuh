@@ -70,7 +70,7 @@ __global__ void __launch_bounds__(kWriteThreads) cache_write_kernel(const CacheW
     x /= p.T;
     const int h = x % p.Hkv, s = x / p.Hkv;
     const int len = p.lengths[s];
-    const int n_new = p.new_lens ? p.new_lens[s] : p.M;
+    const int n_new = p.new_lens ? p.new_lens[s] : (len == 0 ? 0 : p.M);
     if (len < 0 || len > static_cast<long long>(p.nb) * B || n_new < 0 || n_new > p.M || n_new > len) {
         if (threadIdx.x == 0) raise_status(STATUS_BAD_CACHE);
         return;
@@ -274,7 +274,7 @@ __device__ __forceinline__ CachedCell cached_cell(const CachedParams& p, int s, 
     c.len = p.lengths[c.s];
     c.n_new = p.new_lens ? p.new_lens[c.s] : p.M;
     c.list0 = 0;
-    if (c.len < 0 || c.len > static_cast<long long>(p.nb) * B || c.n_new < 0 || c.n_new > p.M || c.n_new > c.len) {
+    if (c.len < 0 || c.len > static_cast<long long>(p.nb) * B || c.n_new < 0 || c.n_new > p.M) {
         raise_status(STATUS_BAD_CACHE);
         c.len = c.n_new = 0;
     }

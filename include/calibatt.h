@@ -367,11 +367,13 @@ calib_status sparse_attn_bwd_repeat(const void* q, const void* k, const void* v,
  *                      Only the first ceil(lengths[s] / B) entries of a row are read.
  *   lengths          : int32 [S], tokens of each sequence, the new ones included; 0 is a free
  *                      slot of the batch.
- *   new_lens         : int32 [S] or NULL (M each): how many of the call's M token slots a
- *                      sequence uses; slot m < new_lens[s] is position lengths[s] -
- *                      new_lens[s] + m.  The slots behind are padding.
- * A length outside [0, max_blocks * B] or a count outside [0, min(M, lengths[s])] leaves that
- * sequence out, a page outside [0, pages) that block; both are reported (calib_device_check).
+ *   new_lens         : int32 [S] or NULL (M each; in calib_cache_write none where lengths[s]
+ *                      is 0): how many of the call's M token slots a sequence uses; slot
+ *                      m < new_lens[s] is position lengths[s] - new_lens[s] + m.  The slots
+ *                      behind are padding.
+ * A length outside [0, max_blocks * B] or a count outside [0, M] (calib_cache_write: also one
+ * above lengths[s]) leaves that sequence out, a page outside [0, pages) that block; both are
+ * reported (calib_device_check).
  * pages * Hkv * B and max_blocks * B are below 2^31 (CALIB_ERR_UNSUPPORTED beyond). */
 
 /* Writes new tokens into the cache.
@@ -402,8 +404,9 @@ int64_t sparse_attn_cached_workspace(int S, int Hq, int Hkv, int M, int D, int b
  *                query heads of K/V head h attend to.  Blocks past the sequence's end are
  *                ignored; `work` is not used.
  *   flags      : CALIB_ATTN_OUT_F32; CALIB_ATTN_CAUSAL: slot m sees the keys at or before its
- *                position (the queries are the sequence's last new_lens[s] tokens).  Without it
- *                every used slot sees all lengths[s] keys.
+ *                position (the queries are the sequence's last new_lens[s] tokens; a slot
+ *                whose position is before the first key sees none).  Without it every used
+ *                slot sees all lengths[s] keys, however many slots there are.
  *   workspace  : 16-byte aligned, sparse_attn_cached_workspace(...) bytes, NULL if that is 0; its
  *                contents need not be set, and one buffer serves one call at a time.
  * Rows without keys (padding slots, free batch slots, nothing kept) write O = 0, LSE = -inf.

@@ -159,7 +159,10 @@ def test_host_tensors_are_refused():
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("H,nq,nk,p", [(1, 1, 1, 1.0), (2, 8, 8, 0.5), (3, 37, 53, 0.3), (2, 31, 33, 1.0),
-                                       (1, 64, 32, 0.0), (40, 158, 591, 0.2), (2, 1500, 40, 0.3), (1, 7, 4000, 0.05)])
+                                       (1, 64, 32, 0.0), (40, 158, 591, 0.2), (2, 1500, 40, 0.3), (1, 7, 4000, 0.05),
+                                       # clusters of 7, 6, 5, 4, 2 and 1 CTAs a head
+                                       (21, 300, 70, 0.4), (24, 260, 33, 0.4), (29, 257, 40, 0.4), (36, 130, 130, 0.3),
+                                       (74, 65, 65, 0.3), (149, 40, 50, 0.3)])
 def test_transpose_exact(H, nq, nk, p):
     rng = np.random.default_rng(H * nq + nk)
     m = (rng.random((H, nq, nk)) < p).astype(np.uint8)

@@ -506,3 +506,24 @@ def test_every_way_of_sharing_the_work(S, Hq, Hkv, M, D, B, longest):
         fin = torch.isfinite(l1[0])
         assert torch.equal(torch.isfinite(lse[s]), fin)
         assert float((lse[s] - l1[0])[fin].abs().max().nan_to_num(0) if fin.any() else 0) <= 2 * n * U32 + 2.0 ** -18
+
+
+@pytest.mark.gpu
+def test_free_slots_and_more_queries_than_keys():
+    """Without new_lens: free slots of a batch write and read nothing and are no error; more query slots than keys see
+    them all (no causal limit) or, causal, only from the first key's position on."""
+    S, H, M, D, B = 3, 2, 6, 64, 64
+    cache, table = _cache(np.random.default_rng(13), S, H, D, B, 2)
+    q = torch.randn(S, H, M, D, generator=torch.Generator().manual_seed(13)).to(torch.bfloat16).cuda()
+    lengths = [4, 0, 70]
+    for causal in (False, True):
+        o, lse = ops.sparse_attn_cached(q, cache, table, _ints(lengths), causal=causal, return_lse=True)
+        ops.device_check()
+        _check(o, lse, q, cache, table, lengths, [M] * S, D ** -0.5, causal)
+        assert torch.isneginf(lse[0, :, :2]).all() == causal
+    x = torch.ones(S, H, 1, D, dtype=torch.bfloat16, device="cuda")
+    before = cache.k.view(torch.uint8)[table[1].long()].clone()
+    ops.cache_write(cache, x, x, table, _ints(lengths))
+    ops.device_check()
+    assert torch.equal(before, cache.k.view(torch.uint8)[table[1].long()])
+    assert float(cache.k[int(table[0, 0]), 0, 3, 0].float() * cache.k_scale[int(table[0, 0]), 0]) != 0
