@@ -125,12 +125,22 @@ def _need(t: torch.Tensor, name: str, dtype: torch.dtype, shape=None):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
-def _on_current_device(*tensors):
-    """The calls launch on the current device's stream, so their tensors have to live there."""
-    dev = torch._C._cuda_getDevice()
-    for t in tensors:
-        if t is not None and t.get_device() != dev:
-            raise ValueError(f"a tensor of this call is on {t.device}, the current device is cuda:{dev}")
+def _need_on(dev: int, t: torch.Tensor, name: str, dtype: torch.dtype, shape=None):
+    """_need, and that t is on device `dev`: the calls launch on the current device's stream."""
+    try:
+        if t.get_device() == dev and t.dtype is dtype and t.is_contiguous() and (shape is None or t.shape == shape):
+            return
+    except AttributeError:
+        pass
+    _need(t, name, dtype, shape)
+    raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
+
+
+def _current_device(t) -> int:
+    """The current CUDA device; refuses host tensors first, with which there may be none."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError("the first argument must be a CUDA tensor")
+    return torch._C._cuda_getDevice()
 
 
 @functools.lru_cache(maxsize=256)
@@ -283,15 +293,15 @@ def mask_to_csr(mask: torch.Tensor):
 def transpose_csr(row_ptr: torch.Tensor, col_idx: torch.Tensor, H: int, nq: int, nk: int):
     """(row_ptr int32 [H*nk+1], col_idx int16) of the skip list by key block: for every (head, key
     block) the ascending query blocks that keep it, with col_idx's capacity."""
-    _need(row_ptr, "row_ptr", torch.int32, (H * nq + 1,))
-    _need(col_idx, "col_idx", torch.int16)
-    _on_current_device(row_ptr, col_idx)
+    dev = _current_device(row_ptr)
+    _need_on(dev, row_ptr, "row_ptr", torch.int32, (H * nq + 1,))
+    _need_on(dev, col_idx, "col_idx", torch.int16)
     t_ptr = row_ptr.new_empty(H * nk + 1)
     t_col = torch.empty_like(col_idx)
     # an empty list still needs valid pointers
     src, dst = (col_idx, t_col) if col_idx.numel() else (row_ptr, t_ptr)
     _check("calib_transpose_csr", lib().calib_transpose_csr(
-        _ptr(row_ptr), _ptr(src), H, nq, nk, _ptr(t_ptr), _ptr(dst), _stream()))
+        row_ptr.data_ptr(), src.data_ptr(), H, nq, nk, t_ptr.data_ptr(), dst.data_ptr(), _stream()))
     return t_ptr, t_col
 
 
@@ -494,34 +504,37 @@ def sparse_attn_fwd_repeat(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, bl
 
 def _bwd(name, q, k, v, out, dout, lse, blist, blist_t, scale, grads, grad_dtype, n_anchor, geometry):
     H, N, D = shape = q.shape
-    bf16 = torch.bfloat16
-    _need(q, "q", bf16)
-    _need(k, "k", bf16, shape)
-    _need(v, "v", bf16, shape)
+    bf16, dev = torch.bfloat16, _current_device(q)
+    _need_on(dev, q, "q", bf16)
+    _need_on(dev, k, "k", bf16, shape)
+    _need_on(dev, v, "v", bf16, shape)
     io = out.dtype
     if io is not bf16 and io is not torch.float32:
         raise TypeError("out must be bf16 or fp32")
-    _need(out, "out", io, shape)
-    _need(dout, "dout", io, shape)
-    _need(lse, "lse", torch.float32, (H, N))
+    _need_on(dev, out, "out", io, shape)
+    _need_on(dev, dout, "dout", io, shape)
+    _need_on(dev, lse, "lse", torch.float32, (H, N))
     if grad_dtype is not bf16 and grad_dtype is not torch.float32:
         raise TypeError("gradients are bf16 or fp32")
     dq, dk, dv = grads
+    new = (lambda: torch.empty_like(q)) if grad_dtype is bf16 else (lambda: torch.empty_like(q, dtype=grad_dtype))
     if dq is None:
-        dq = torch.empty_like(q, dtype=grad_dtype)
+        dq = new()
     else:
-        _need(dq, "dq", grad_dtype, shape)
+        _need_on(dev, dq, "dq", grad_dtype, shape)
     if dk is None:
-        dk = torch.empty_like(q, dtype=grad_dtype)
+        dk = new()
     else:
-        _need(dk, "dk", grad_dtype, shape)
+        _need_on(dev, dk, "dk", grad_dtype, shape)
     if dv is None:
-        dv = torch.empty_like(q, dtype=grad_dtype)
+        dv = new()
     else:
-        _need(dv, "dv", grad_dtype, shape)
+        _need_on(dev, dv, "dv", grad_dtype, shape)
     if blist_t is None:
         blist_t = blist.transpose()
-    _on_current_device(q, k, v, out, dout, lse, dq, dk, dv, blist.row_ptr, blist_t.row_ptr)
+    for bl in (blist, blist_t):
+        if bl.row_ptr.get_device() != dev:
+            raise ValueError(f"a skip list is on {bl.row_ptr.device}, the current device is cuda:{dev}")
     flags = (CALIB_ATTN_OUT_F32 if io is torch.float32 else 0) | \
         (CALIB_ATTN_GRAD_F32 if grad_dtype is torch.float32 else 0)
     need = _workspace_bytes("sparse_attn_bwd_workspace", H, N, D, blist.block, n_anchor, flags)
@@ -619,40 +632,46 @@ class KVCache:
         scale = lambda: torch.zeros((pages, Hkv), dtype=torch.float32, device=device)
         return KVCache(data(), data(), scale(), scale())
 
-    def check(self):
-        """(pages, Hkv, block, D) of a well-formed cache; raises otherwise."""
-        pages, Hkv, block, D = shape = self.k.shape
-        _need(self.k, "cache.k", torch.float8_e4m3fn)
-        _need(self.v, "cache.v", torch.float8_e4m3fn, shape)
-        _need(self.k_scale, "cache.k_scale", torch.float32, (pages, Hkv))
-        _need(self.v_scale, "cache.v_scale", torch.float32, (pages, Hkv))
-        return pages, Hkv, block, D
+    def check(self, dev: int):
+        """Shape (pages, Hkv, block, D) of a well-formed cache on device `dev`; raises otherwise."""
+        shape = self.k.shape
+        if len(shape) != 4:
+            raise ValueError(f"cache.k must have shape [pages, Hkv, block, D], got {tuple(shape)}")
+        _need_on(dev, self.k, "cache.k", torch.float8_e4m3fn)
+        _need_on(dev, self.v, "cache.v", torch.float8_e4m3fn, shape)
+        _need_on(dev, self.k_scale, "cache.k_scale", torch.float32, shape[:2])
+        _need_on(dev, self.v_scale, "cache.v_scale", torch.float32, shape[:2])
+        return shape
 
 
-def _sequences(block_table, lengths, new_lens, S):
-    _need(block_table, "block_table", torch.int32)
-    if block_table.dim() != 2 or block_table.shape[0] != S:
-        raise ValueError(f"block_table must have shape ({S}, max_blocks), got {tuple(block_table.shape)}")
-    _need(lengths, "lengths", torch.int32, (S,))
+def _sequences(dev, block_table, lengths, new_lens, S):
+    _need_on(dev, block_table, "block_table", torch.int32)
+    shape = block_table.shape
+    if len(shape) != 2 or shape[0] != S:
+        raise ValueError(f"block_table must have shape ({S}, max_blocks), got {tuple(shape)}")
+    _need_on(dev, lengths, "lengths", torch.int32, (S,))
     if new_lens is not None:
-        _need(new_lens, "new_lens", torch.int32, (S,))
-    return block_table.shape[1]
+        _need_on(dev, new_lens, "new_lens", torch.int32, (S,))
+    return shape[1]
 
 
 def cache_write(cache: KVCache, k_new: torch.Tensor, v_new: torch.Tensor, block_table: torch.Tensor,
                 lengths: torch.Tensor, new_lens: Optional[torch.Tensor] = None) -> KVCache:
     """Write new tokens k_new, v_new (bf16 [S, Hkv, M, D]) into the cache, in place: slot m of
     sequence s goes to position lengths[s] - new_lens[s] + m (new_lens: M each by default)."""
-    pages, Hkv, block, D = cache.check()
-    S, M = k_new.shape[0], k_new.shape[2] if k_new.dim() == 4 else 0
+    dev = _current_device(k_new)
+    pages, Hkv, block, D = cache.check(dev)
+    if k_new.dim() != 4:
+        raise ValueError("k_new must have shape [S, Hkv, M, D]")
+    S, _, M, _ = k_new.shape
     shape = (S, Hkv, M, D)
-    _need(k_new, "k_new", torch.bfloat16, shape)
-    _need(v_new, "v_new", torch.bfloat16, shape)
-    nb = _sequences(block_table, lengths, new_lens, S)
-    _on_current_device(k_new, v_new, cache.k, cache.v, cache.k_scale, cache.v_scale, block_table, lengths, new_lens)
+    _need_on(dev, k_new, "k_new", torch.bfloat16, shape)
+    _need_on(dev, v_new, "v_new", torch.bfloat16, shape)
+    nb = _sequences(dev, block_table, lengths, new_lens, S)
     _check("calib_cache_write", lib().calib_cache_write(
-        _ptr(k_new), _ptr(v_new), _ptr(cache.k), _ptr(cache.v), _ptr(cache.k_scale), _ptr(cache.v_scale),
-        _ptr(block_table), _ptr(lengths), _ptr(new_lens), S, Hkv, M, D, block, nb, pages, _stream()))
+        k_new.data_ptr(), v_new.data_ptr(), cache.k.data_ptr(), cache.v.data_ptr(), cache.k_scale.data_ptr(),
+        cache.v_scale.data_ptr(), block_table.data_ptr(), lengths.data_ptr(), _ptr(new_lens), S, Hkv, M, D, block, nb, pages,
+        _stream()))
     return cache
 
 
@@ -665,34 +684,37 @@ def sparse_attn_cached(q: torch.Tensor, cache: KVCache, block_table: torch.Tenso
     cached keys and values, over all of a sequence's blocks or those that blist (H = Hkv, nq = S,
     nk = max_blocks) keeps.  O [S, Hq, M, D] in bf16 (or fp32 via out_dtype / an fp32 `out`), and the fp32
     LSE [S, Hq, M] if requested."""
-    pages, Hkv, block, D = cache.check()
-    if q.dim() != 4:
-        raise ValueError("q must have shape [S, Hq, M, D]")
-    S, Hq, M, _ = q.shape
-    _need(q, "q", torch.bfloat16, (S, Hq, M, D))
-    nb = _sequences(block_table, lengths, new_lens, S)
+    dev = _current_device(q)
+    pages, Hkv, block, D = cache.check(dev)
+    shape = q.shape
+    if len(shape) != 4 or shape[3] != D:
+        raise ValueError(f"q must have shape [S, Hq, M, {D}], got {tuple(shape)}")
+    S, Hq, M, _ = shape
+    _need_on(dev, q, "q", torch.bfloat16)
+    nb = _sequences(dev, block_table, lengths, new_lens, S)
     if out is not None:
         out_dtype = out.dtype
     if out_dtype is not torch.bfloat16 and out_dtype is not torch.float32:
         raise TypeError("out must be bf16 or fp32")
     if out is None:
-        out = torch.empty_like(q, dtype=out_dtype)
+        out = torch.empty_like(q) if out_dtype is torch.bfloat16 else torch.empty_like(q, dtype=out_dtype)
     else:
-        _need(out, "out", out_dtype, (S, Hq, M, D))
+        _need_on(dev, out, "out", out_dtype, shape)
     if lse is not None:
-        _need(lse, "lse", torch.float32, (S, Hq, M))
+        _need_on(dev, lse, "lse", torch.float32, shape[:3])
     elif return_lse:
-        lse = q.new_empty((S, Hq, M), dtype=torch.float32)
-    _on_current_device(q, cache.k, cache.v, cache.k_scale, cache.v_scale, block_table, lengths, new_lens, out, lse,
-                       None if blist is None else blist.row_ptr)
+        lse = q.new_empty(shape[:3], dtype=torch.float32)
+    if blist is not None and blist.row_ptr.get_device() != dev:
+        raise ValueError(f"the skip list is on {blist.row_ptr.device}, the current device is cuda:{dev}")
     need = _workspace_bytes("sparse_attn_cached_workspace", S, Hq, Hkv, M, D, block, nb)
     space = q.new_empty(need, dtype=torch.uint8) if need > 0 else None
     cs = None if blist is None else blist.c_struct()
     flags = (CALIB_ATTN_OUT_F32 if out_dtype is torch.float32 else 0) | (CALIB_ATTN_CAUSAL if causal else 0)
     scale = 1.0 / math.sqrt(D) if scale is None else scale
     _check("sparse_attn_cached", lib().sparse_attn_cached(
-        _ptr(q), _ptr(cache.k), _ptr(cache.v), _ptr(cache.k_scale), _ptr(cache.v_scale), _ptr(block_table),
-        _ptr(lengths), _ptr(new_lens), _ptr(out), _ptr(lse), S, Hq, Hkv, M, D, block, nb, pages, scale,
+        q.data_ptr(), cache.k.data_ptr(), cache.v.data_ptr(), cache.k_scale.data_ptr(), cache.v_scale.data_ptr(),
+        block_table.data_ptr(), lengths.data_ptr(), _ptr(new_lens), out.data_ptr(), _ptr(lse), S, Hq, Hkv, M, D, block, nb,
+        pages, scale,
         None if cs is None else ctypes.byref(cs), flags, _ptr(space), max(0, need), _stream()))
     return (out, lse) if (return_lse or lse is not None) else out
 
