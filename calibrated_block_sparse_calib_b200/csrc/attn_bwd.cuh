@@ -61,7 +61,9 @@ __device__ __forceinline__ int anchor_copies(const AttnParams& p, int a) {
 // row, and the operands that the products need as bf16: dO when it came as fp32, and for a repeat head the
 // anchors' rows of Q with dO and delta summed over the tokens that take the anchor's output (its O
 // and LSE are the same in all of them).  The sum is fp32 and dO enters the products as bf16, so it
-// is rounded once (2^-8 relative at most), as P and dS are.  Rows past the sequence get -LSE = -inf, which
+// is rounded once (2^-8 relative at most), as P and dS are.  delta is then taken from the rounded values: the
+// result is the gradient for that dO, and the rounding's part along O cancels in dP - delta instead of adding up over a
+// row's keys.  Rows past the sequence get -LSE = -inf, which
 // makes their probabilities 0; so do rows with nothing kept.
 // Reads dO and O once: 2 x 268 MB at 12 x 32760 x 128, bound by memory.
 template <int D>
@@ -78,12 +80,13 @@ __global__ void __launch_bounds__(256) bwd_prepare_kernel(const BwdParams p, int
     if (r < Nq) {
         const int tok = rep ? anchor_token(g, r) : r;
         const int n = rep ? anchor_copies(g, r) : 1;
-        float dsum[8];
+        const bool rounds = rep || p.io_f32;
+        float dsum[8], b[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) dsum[e] = 0.f;
         for (int c = 0; c < n; ++c) {
             const size_t at = (static_cast<size_t>(h) * g.N + tok + static_cast<size_t>(c) * g.Wl) * D + part * 8;
-            float a[8], b[8];
+            float a[8];
             if (p.io_f32) {
                 const float4* x = reinterpret_cast<const float4*>(static_cast<const float*>(p.dout) + at);
                 const float4* y = reinterpret_cast<const float4*>(static_cast<const float*>(p.o) + at);
@@ -103,14 +106,17 @@ __global__ void __launch_bounds__(256) bwd_prepare_kernel(const BwdParams p, int
                 }
             }
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                acc += a[e] * b[e];
-                dsum[e] += a[e];
-            }
+            for (int e = 0; e < 8; ++e) dsum[e] += a[e];
         }
-        if (rep || p.io_f32) {
+        if (rounds) {
             const uint4 w = make_uint4(pack_bf16x2(dsum[0], dsum[1]), pack_bf16x2(dsum[2], dsum[3]),
                                        pack_bf16x2(dsum[4], dsum[5]), pack_bf16x2(dsum[6], dsum[7]));
+            const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                dsum[2 * e] = __uint_as_float(ws[e] << 16);
+                dsum[2 * e + 1] = __uint_as_float(ws[e] & 0xFFFF0000u);
+            }
             if (rep) {
                 const size_t to = (static_cast<size_t>(h) * g.n_anchor + r) * D + part * 8;
                 *reinterpret_cast<uint4*>(p.doa + to) = w;
@@ -120,6 +126,8 @@ __global__ void __launch_bounds__(256) bwd_prepare_kernel(const BwdParams p, int
                 *reinterpret_cast<uint4*>(p.do16 + (static_cast<size_t>(h) * g.N + r) * D + part * 8) = w;
             }
         }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc += dsum[e] * b[e];
         const float l = p.lse[static_cast<size_t>(h) * g.N + tok];
         if (l != -INFINITY) nlse = -l * 1.4426950408889634f;
     }

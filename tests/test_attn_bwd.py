@@ -11,7 +11,7 @@ value), fp32 sums, and the result rounded once:
 where u = 2^-8, e = the relative error of P = exp(S - LSE) plus the sums' (D + 8) 2^-24 max|scale q||k|
 + N 2^-24 + 2^-20 (the exponential), d = (D + 8) 2^-24 (|do||v|^T + sum|do||o|) is the error of dP - delta,
 and u_out = 2^-8 for bf16 results, 2^-24 for fp32 ones.  An fp32 dout, or a repeat head's summed one,
-is itself rounded to bf16: then do carries another u (u |P|^T|do| in dv, u |do||v|^T in d).
+is itself rounded to bf16: then do carries another u (u |P|^T|do| in dv, u (|do||v|^T + sum|do||o|) in d).
 That bound adds every rounding up as if all were largest and of one sign; the roundings' expected
 squares (a value off by at most u |x| has a mean square of at most u^2 x^2 / 3 over the positions in a
 step) give the second check, ||err|| <= 2 sqrt(expected), which a wrong term in a few hundred fails.
@@ -211,7 +211,8 @@ def _bounds(q, k, v, o, do, lse, scale, B, mask, u_do):
     size = scale * np.abs(q) @ np.abs(k).T
     e = (D + 8) * U32 * size.max(initial=0.0) + max(N, Nq) * U32 + 2.0 ** -20
     d32 = (D + 8) * U32 * (np.abs(do) @ np.abs(v).T + (np.abs(do) * np.abs(o)).sum(1)[:, None])
-    d = d32 + u_do * (np.abs(do) @ np.abs(v).T)
+    # a rounded do moves dP and delta (which is taken from it) together: by sum_d |do_d| u |v_d - o_d| at most
+    d = d32 + u_do * (np.abs(do) @ np.abs(v).T + (np.abs(do) * np.abs(o)).sum(1)[:, None])
     # what is below the smallest normal number, 2^-126, may become 0: each P loses that much at most, and each dS
     # that times |dP - delta| and once more for its own size
     least = 2.0 ** -126 * keep
