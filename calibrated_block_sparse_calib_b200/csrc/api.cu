@@ -199,9 +199,10 @@ calib_status attn_prepare(const void* q, const void* k, const void* v, void* o, 
     c->D = D;
     c->B = B;
     c->grid = list->work ? list->n_work : H * nb;
-    if (!make_tmap(&c->tk, k, D, N, H, B) || !make_tmap(&c->tv, v, D, N, H, B) ||
-        !make_tmap(&c->tq, q, D, N, H, B) || !make_tmap(&c->tq1, q, D, N, H, 1))
+    if (!make_tmap(&c->tk, k, D, N, H, B) || !make_tmap(&c->tv, v, D, N, H, B) || !make_tmap(&c->tq, q, D, N, H, B))
         return CALIB_ERR_CUDA;
+    c->tq1 = c->tq;                 // single rows are gathered for repeat heads only
+    if (repeat_bits && !make_tmap(&c->tq1, q, D, N, H, 1)) return CALIB_ERR_CUDA;
     return CALIB_OK;
 }
 
@@ -359,10 +360,10 @@ BwdSpace bwd_space(int H, int N, int D, int B, long long n_anchor, bool io_f32) 
 
 template <int D, int BLK>
 calib_status launch_bwd(const calib::BwdMaps& m, const calib::BwdParams& p, cudaStream_t st) {
-    // ring depth: what fits beside the two resident tiles (194 KB at D = B = 128, at most 194 KB elsewhere)
+    // ring depth: what fits beside the two resident tiles (at most 194 KB; 98 KB at D = B = 64, two CTAs an SM)
     constexpr int ST = D == 128 && BLK == 128 ? 2 : 4;
     using L = calib::BwdSmem<D, BLK, ST>;
-    static_assert(L::BYTES <= 232448, "shared memory budget");
+    static_assert(L::BYTES + 1024 <= 233472 / calib::bwd_ctas(D, BLK), "shared memory budget");
     const int rows = p.geo.nq * BLK;
     const long long threads = static_cast<long long>(p.geo.H) * rows * (D / 8);
     auto* fn = calib::bwd_kernel<D, BLK, ST>;

@@ -139,26 +139,31 @@ __global__ void __launch_bounds__(256) bwd_prepare_kernel(const BwdParams p, int
     }
 }
 
-// Arithmetic warps, four for each part of a tile's columns (one per 32 TMEM lanes).
-constexpr int kBwdParts = 4;
-constexpr int bwd_parts(int blk) { return blk == 128 ? kBwdParts : 2; }
-constexpr int bwd_threads(int blk) { return 64 + 128 * bwd_parts(blk); }   // warp 0 TMA, warp 1 MMA
+// CTAs per SM.  At D = 64 with blocks of 64 a tile's products are short next to its loads, exponentials and
+// hand-overs and a CTA's start and end, so two CTAs share an SM (256 tensor-memory columns each) and fill each
+// other's gaps: 2 x 16384 x 64 dense 1627 -> 1100 us, 16 x 1024 x 64 88 -> 62 us.  (Blocks of 128 taken as two
+// halves in this way: 581 -> 575 us, but 85 -> 94 us on 6 x 4999 x 64, whose items are then half as many as places.)
+__host__ __device__ constexpr int bwd_ctas(int d, int blk) { return d == 64 && blk == 64 ? 2 : 1; }
+// Arithmetic warps: four (one per 32 TMEM lanes) for each part of a tile's columns.
+__host__ __device__ constexpr int bwd_parts(int blk) { return blk == 128 ? 4 : 2; }
+__host__ __device__ constexpr int bwd_threads(int blk) { return 64 + 128 * bwd_parts(blk); }   // warp 0 TMA, warp 1 MMA
 
 // Tensor-memory columns: S and dP (fp32, BLK columns each), P and dS (bf16 pairs, BLK / 2 each), the
-// accumulators (D each) and, for dQ, Q and dO (bf16 pairs, D / 2 each).  All of it fits 512 columns except
-// at D = BLK = 128; there P overwrites S and dS overwrites dP, each part's columns by the warp that
+// accumulators (D each) and, for dQ, Q and dO (bf16 pairs, D / 2 each).  Where a CTA's columns do not hold all of it
+// (D = BLK = 128 and D = BLK = 64), P overwrites S and dS overwrites dP, each part's columns by the warp that
 // loaded them, and the next S (dP) waits for the product that reads P (dS).  STEP: columns between two
 // parts of P or dS.
 template <int D, int BLK>
 struct BwdTmem {
-    static constexpr bool SEP = 3 * BLK + 2 * D <= 512;
+    static constexpr int COLS = 512 / bwd_ctas(D, BLK);
+    static constexpr bool SEP = 3 * BLK + 2 * D <= COLS;
     static constexpr uint32_t S = 0, DP = BLK;
     static constexpr int NP = bwd_parts(BLK), HC = BLK / NP;   // parts of a tile's columns, columns each
     static constexpr uint32_t P = SEP ? 2 * BLK : S, STEP = SEP ? HC / 2 : HC;
     static constexpr uint32_t DS = SEP ? 2 * BLK + BLK / 2 : DP;
     static constexpr uint32_t ACC = SEP ? 3 * BLK : 2 * BLK;
     static constexpr uint32_t Q = ACC + D, DO = Q + D / 2;
-    static_assert(ACC + 2 * D <= 512, "tensor memory");
+    static_assert(ACC + 2 * D <= COLS, "tensor memory");
 };
 
 // (d0, d1) = (a0, a1) * (b0, b1), packed fp32x2
@@ -254,9 +259,9 @@ struct BwdSmem {
                          B_SE = B_SF + 1, B_DPF = B_SE + 1, B_DPE = B_DPF + 1, B_PF = B_DPE + 1, B_DSF = B_PF + 1, B_END = B_DSF + 1,
                          B_DRAIN = B_END + 1, NBARS = B_DRAIN + 1;
     static constexpr uint32_t OFF_MISC = OFF_BAR + NBARS * 8;
-    // + alignment slack; at least 120 KB, so that one CTA (all 512 TMEM columns) is resident per SM
-    static constexpr uint32_t RAW = OFF_MISC + 16 + 1024;
-    static constexpr uint32_t BYTES = RAW > 120u * 1024 ? RAW : 120u * 1024;
+    // + alignment slack; at least what keeps more CTAs off an SM than its tensor memory is cut for
+    static constexpr uint32_t RAW = OFF_MISC + 16 + 1024, LEAST = (bwd_ctas(D, BLK) == 1 ? 120u : 80u) * 1024;
+    static constexpr uint32_t BYTES = RAW > LEAST ? RAW : LEAST;
 };
 
 // dK and dV of one key block, over the query blocks that keep it.  With the keys as the rows of
@@ -314,7 +319,7 @@ __device__ __forceinline__ void bwd_kv(const BwdMaps& m, const BwdParams& p, int
         fence_barrier_init();
     }
     if (warp == 1) {
-        tmem_alloc(smem_u32(tmem_slot), kTmemCols);
+        tmem_alloc(smem_u32(tmem_slot), T::COLS);
         tmem_relinquish();
     }
     tc_fence_before();
@@ -557,7 +562,7 @@ __device__ __forceinline__ void bwd_kv(const BwdMaps& m, const BwdParams& p, int
     __syncthreads();
     if (warp == 1) {
         tc_fence_after();
-        tmem_dealloc(tmem, kTmemCols);
+        tmem_dealloc(tmem, T::COLS);
     }
 }
 
@@ -613,7 +618,7 @@ __device__ __forceinline__ void bwd_q(const BwdMaps& m, const BwdParams& p, int 
         fence_barrier_init();
     }
     if (warp == 1) {
-        tmem_alloc(smem_u32(tmem_slot), kTmemCols);
+        tmem_alloc(smem_u32(tmem_slot), T::COLS);
         tmem_relinquish();
     }
     tc_fence_before();
@@ -838,14 +843,14 @@ __device__ __forceinline__ void bwd_q(const BwdMaps& m, const BwdParams& p, int 
     __syncthreads();
     if (warp == 1) {
         tc_fence_after();
-        tmem_dealloc(tmem, kTmemCols);
+        tmem_dealloc(tmem, T::COLS);
     }
 }
 
 // Both gradients in one launch: the key blocks' items first (four products a tile), then the query blocks'
 // (three), which fill the SMs that run out of the former.
 template <int D, int BLK, int ST>
-__global__ void __launch_bounds__(bwd_threads(BLK), 1) bwd_kernel(const __grid_constant__ BwdMaps m, const __grid_constant__ BwdParams p) {
+__global__ void __launch_bounds__(bwd_threads(BLK), bwd_ctas(D, BLK)) bwd_kernel(const __grid_constant__ BwdMaps m, const __grid_constant__ BwdParams p) {
     const int n_kv = p.geo.H * p.geo.nk;
     const int id = static_cast<int>(blockIdx.x);
     if (id < n_kv) bwd_kv<D, BLK, ST>(m, p, id);
