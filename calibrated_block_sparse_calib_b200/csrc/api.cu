@@ -727,9 +727,10 @@ calib_status calib_transpose_csr(const int32_t* row_ptr, const int16_t* col_idx,
     const int cluster = std::max(1, std::min(std::min(kSms / H, calib::kTransMaxCluster), words));
     const int per = cdiv(words, cluster), stride = per | 1;
     const int cols = std::min(std::min(nk, calib::kTransThreads), 80 * 1024 / 4 / stride);
-    const int bytes = std::max(116 * 1024, (cols * stride + per * 32) * 4);
+    constexpr int stage = calib::kTransWarps * 4 * calib::kTransStage * 2;
+    const int bytes = std::max(116 * 1024, cols * stride * 4 + stage + per * 32 * 2);
     auto* fn = calib::transpose_csr_kernel;
-    if (calib_status s = ensure_smem(reinterpret_cast<const void*>(fn), 80 * 1024 + 32768 * 4)) return s;
+    if (calib_status s = ensure_smem(reinterpret_cast<const void*>(fn), 80 * 1024 + stage + 32768 * 2)) return s;
     return launch_with(fn, H * cluster, calib::kTransThreads, bytes, as_stream(stream), cluster, false, row_ptr, col_idx, nq,
                        nk, cluster, cols, t_row_ptr_out, t_col_idx_out);
 }

@@ -56,10 +56,12 @@ constexpr int kWriteThreads = 256;
 // then rounded again at the new one (a second rounding, up to half an e4m3 step); if it does not
 // grow their bytes stay.  So the largest value of a block is never cut off, and one token costs one
 // row, not its block.  Bytes at and behind the sequence's end are left as they were.
-// Bound by memory: 2 bytes in and 1 out per value (8 prompts of up to 4096 tokens, 8 heads, 101 MB: 22.6 us,
-// 4.5 TB/s).  A CTA per block and head, so that the largest magnitude needs one barrier and the tokens one load.
+// Bound by memory: 2 bytes in and 1 out per value (8 prompts of up to 4096 tokens, 8 heads, about
+// 101 MB: 21.4 us; 25.0 us with the two CTAs per SM that the registers would allow unasked, 21.6 with five).  A CTA per
+// block and head, so that the largest magnitude needs one barrier and the tokens one load; four CTAs overlap
+// one's loads with another's barrier and stores.
 template <int D, int B>
-__global__ void __launch_bounds__(kWriteThreads) cache_write_kernel(const CacheWriteParams p) {
+__global__ void __launch_bounds__(kWriteThreads, 4) cache_write_kernel(const CacheWriteParams p) {
     constexpr int CPR = D / 8;                             // 8-value chunks per token
     constexpr int PER = B * CPR / kWriteThreads;           // chunks per thread (4 or 8 or 2)
     __shared__ float red[kWriteThreads / 32];

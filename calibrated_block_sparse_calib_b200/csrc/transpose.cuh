@@ -11,13 +11,14 @@
 //     other's counts through distributed shared memory, which gives every column's total, its prefix
 //     and this CTA's place in it.  A head has as many entries in either order, so its columns start
 //     at row_ptr[h*nq], whatever other heads do;
-//   - one warp per column writes out the set bits' indices, a word's 32 rows side by side.
+//   - a warp takes four columns, eight lanes each with a word of 32 rows a lane, turns the set bits
+//     into indices in shared memory and writes those out side by side.
 // Integer work; bits are set in any order and read in one: the result is exact and the same in
 // every run.
-// What bounds it is instructions, most of them in the writing (a column has few words per CTA);
-// the 14 MB that a 40 x 591 x 591 list at 25% reads and writes would take 2.2 us of HBM time.
+// What bounds it is instructions, of the reading and the writing in about equal parts; the 14 MB that a 40 x 591 x 591 list at 25% reads and writes would take 2.2 us of HBM time.
 // Measured there: 46 us with a bisection per row and 32 columns a CTA, 39 us with every row read by the
-// CTAs of each 128 columns, 29 us as it is; 6 us at 12 x 64 x 64 (graph replays).
+// CTAs of each 128 columns, 29 us with clusters and a warp per column, 25 us as it is; 6 us at 12 x 64 x 64
+// (graph replays).
 #pragma once
 #include "ptx.cuh"
 #include "select.cuh"
@@ -27,18 +28,21 @@ namespace calib {
 constexpr int kTransThreads = 1024;
 constexpr int kTransWarps = kTransThreads / 32;
 constexpr int kTransMaxCluster = 8;
+constexpr int kTransStage = 8 * 32;       // indices of a column that a warp holds at a time: eight words' rows
 
 __global__ void __launch_bounds__(kTransThreads)
 transpose_csr_kernel(const int32_t* __restrict__ row_ptr, const int16_t* __restrict__ col_idx, int nq, int nk,
                      int cluster, int cols, int32_t* __restrict__ t_row_ptr, int16_t* __restrict__ t_col_idx) {
-    // words of this CTA's rows per column (odd stride: neighbouring columns on different banks), then the rows' cursors
+    // words of this CTA's rows per column (odd stride: neighbouring columns on different banks), a warp's indices, and how
+    // far each row has been read
     extern __shared__ uint32_t bits[];
     __shared__ int32_t count[kTransThreads], first[kTransThreads], warp_sum[kTransWarps];
     const int h = static_cast<int>(blockIdx.x) / cluster, rank = static_cast<int>(blockIdx.x) - h * cluster;
     const int per = ((nq + 31) / 32 + cluster - 1) / cluster;              // words per CTA
     const int i0 = min(nq, rank * per * 32), rows = min(nq, i0 + per * 32) - i0;
     const int words = (rows + 31) / 32, stride = per | 1;
-    int32_t* cursor = reinterpret_cast<int32_t*>(bits + cols * stride);
+    int16_t* stage = reinterpret_cast<int16_t*>(bits + cols * stride) + warp_id() * 4 * kTransStage;
+    uint16_t* cursor = reinterpret_cast<uint16_t*>(bits + cols * stride + kTransWarps * 4 * kTransStage / 2);
     const int warp = static_cast<int>(warp_id()), lane = static_cast<int>(lane_id()), tid = static_cast<int>(threadIdx.x);
     const int32_t* rp = row_ptr + static_cast<size_t>(h) * nq + i0;
     int base = row_ptr[static_cast<size_t>(h) * nq];
@@ -55,7 +59,7 @@ transpose_csr_kernel(const int32_t* __restrict__ row_ptr, const int16_t* __restr
                 if (lane == 0 && j0 == 0) raise_status(STATUS_BAD_LIST);
                 end = beg;
             }
-            int x = j0 == 0 ? beg : cursor[i];
+            int x = j0 == 0 ? beg : min(end, beg + cursor[i]);
             const uint32_t bit = 1u << (i & 31);
             uint32_t* word = bits + (i >> 5);
             while (x < end) {
@@ -71,7 +75,7 @@ transpose_csr_kernel(const int32_t* __restrict__ row_ptr, const int16_t* __restr
                 x += here;
                 if (here < 128) break;                     // an entry behind the tile, or the row's end
             }
-            if (lane == 0 && j1 < nk) cursor[i] = x;
+            if (lane == 0 && j1 < nk) cursor[i] = static_cast<uint16_t>(x - beg);
         }
         __syncthreads();
         if (tid < n_cols) {
@@ -104,12 +108,34 @@ transpose_csr_kernel(const int32_t* __restrict__ row_ptr, const int16_t* __restr
         }
         base += __reduce_add_sync(0xffffffffu, sums);
         __syncthreads();
-        for (int c = warp; c < n_cols; c += kTransWarps) {
-            int out = first[c];
-            for (int w = 0; w < words; ++w) {
-                const uint32_t word = bits[c * stride + w];
-                if ((word >> lane) & 1u) t_col_idx[out + __popc(word & lanemask_lt())] = static_cast<int16_t>(i0 + w * 32 + lane);
-                out += __popc(word);
+        for (int c0 = warp * 4; c0 < n_cols; c0 += kTransWarps * 4) {
+            const int sub = lane >> 3, c = c0 + sub;
+            int out = c < n_cols ? first[c] : 0;
+            for (int w0 = 0; w0 < words; w0 += 8) {
+                const int w = w0 + (lane & 7);
+                uint32_t word = c < n_cols && w < words ? bits[c * stride + w] : 0u;
+                const int own = __popc(word);
+                int incl = own;
+#pragma unroll
+                for (int off = 1; off < 8; off <<= 1) {
+                    const int y = __shfl_up_sync(0xffffffffu, incl, off, 8);
+                    if ((lane & 7) >= off) incl += y;
+                }
+                int16_t* to = stage + sub * kTransStage + incl - own;
+                const int row = i0 + w * 32;
+                while (word) {
+                    *to++ = static_cast<int16_t>(row + __ffs(word) - 1);
+                    word &= word - 1;
+                }
+                const int total = __shfl_sync(0xffffffffu, incl, 7, 8);
+                __syncwarp();
+#pragma unroll
+                for (int v = 0; v < 4; ++v) {
+                    const int n = __shfl_sync(0xffffffffu, total, v * 8), at = __shfl_sync(0xffffffffu, out, v * 8);
+                    for (int x = lane; x < n; x += 32) t_col_idx[at + x] = stage[v * kTransStage + x];
+                }
+                __syncwarp();
+                out += total;
             }
         }
         cluster_barrier();                                 // the counts are read, and the bits of every warp's columns
