@@ -58,6 +58,7 @@ __device__ __forceinline__ uint32_t cluster_rank() {
     return r;
 }
 __device__ __forceinline__ void cluster_barrier() {
+    __syncwarp();                                          // .aligned: the warp's threads come together
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 __device__ __forceinline__ float4 cluster_load(uint32_t addr, uint32_t rank) {

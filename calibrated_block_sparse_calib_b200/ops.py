@@ -101,6 +101,8 @@ def _check(fn: str, s: int):
 
 
 def _stream():
+    if not torch.cuda.is_initialized():
+        torch.cuda.init()
     return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 

@@ -2,6 +2,8 @@
 slice, train through its list, write the trained keys and values into a cache and attend to them token by token
 under the same mask.  Tolerances as in test_attn_bwd.py and test_kv_cache.py, whose checks are used."""
 import math
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -10,9 +12,9 @@ import torch
 import oracle
 import test_attn_bwd
 import test_kv_cache
-from calibrated_block_sparse_calib_b200 import ops, synth
+from calibrated_block_sparse_calib_b200 import ops
 from calibrated_block_sparse_calib_b200.calibrate import calibrate_slice
-from conftest import to64
+from conftest import ROOT, to64
 
 pytestmark = pytest.mark.gpu
 
@@ -142,3 +144,10 @@ def test_the_first_cuda_call_of_a_thread(which):
     t.join()
     assert not raised, raised
     ops.device_check()
+
+
+def test_the_first_cuda_call_of_a_process():
+    """A call that takes no tensor, before anything else has touched CUDA."""
+    body = "from calibrated_block_sparse_calib_b200 import ops; ops.device_check(); print('ok')"
+    res = subprocess.run([sys.executable, "-c", body], capture_output=True, text=True, timeout=240, cwd=ROOT)
+    assert res.returncode == 0 and res.stdout.strip() == "ok", res.stderr[-2000:]
