@@ -6,6 +6,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 #include <type_traits>
@@ -25,6 +26,7 @@
 #include "transpose.cuh"
 #include "attn_bwd.cuh"
 #include "kv_cache.cuh"
+#include "kv_cache_wide.cuh"
 
 namespace {
 
@@ -433,13 +435,19 @@ calib_status bwd_common(const void* q, const void* k, const void* v, const void*
 }
 
 // ---- 8-bit cache -------------------------------------------------------------------
-// How a call's work is shared (see cached_attn_kernel): rows per unit (8 or 16), units per K/V head, and `flat`:
+// How a call's work is shared (see cached_attn_kernel): rows per unit (8, 16 or 128), units per K/V head, and `flat`:
 // shares per K/V head and row tile, or 0 for a cluster per unit and no second launch.  Clusters where no sequence
 // can be longer than 2048 keys (5 to 8 steps for each of a CTA's warps, about what the cut's merge costs), or
 // 8192 if the GPU has room for clusters of 8, or where the units fill the GPU 8 times and more; a cluster has one step
 // for each of its warps, as far as 8 CTAs and the GPU's places go.  The number of shares is the one that takes the
 // fewest steps in all if every sequence is as long as the table allows: rounds of CTAs times a share's steps and 6
 // more for its start and end.
+//
+// cached_wide_kernel takes many query rows.  Its 128 rows cost what 2 tiles of 16 rows (4 at D = 64) cost
+// cached_attn_kernel (4 sequences of 65536 keys, 8 K/V heads: 242 against 228 us with 32 rows and 241 against 332 with
+// 40 at D = 128; 235 against 236 with 64 at D = 64), and about 10 us more to start and end, which 2^18 keys times tiles
+// saved (2^19 at D = 64) make up for: 2 x 1024 keys, 4 heads, 256 rows, 29 against 20 us; 16 x 2048 keys, 8 heads, 40
+// rows, 54 against 64.
 struct CachedPlan {
     int nt, tiles, flat, cluster;
     long long units, grid;
@@ -448,23 +456,27 @@ struct CachedPlan {
 CachedPlan cached_plan(int S, int Hq, int Hkv, int M, int D, int B, int nb) {
     CachedPlan c{};
     const long long rows = static_cast<long long>(Hq / Hkv) * M;
-    c.nt = rows <= 8 ? 1 : 2;
+    const long long keys = static_cast<long long>(nb) * B;
+    const long long saved = cdiv(rows, 16) - (D == 128 ? 2 : 4) * static_cast<long long>(cdiv(rows, calib::kWideRows));
+    const bool wide = saved > 0 && static_cast<double>(S) * Hkv * static_cast<double>(keys) * static_cast<double>(saved) >=
+                                       (D == 128 ? 262144. : 524288.);
+    c.nt = rows <= 8 ? 1 : (wide ? calib::kWideRows / 8 : 2);
     c.tiles = cdiv(rows, 8 * c.nt);
     const long long columns = static_cast<long long>(Hkv) * c.tiles;
     c.units = S * columns;
     c.grid = c.units;
-    const long long places = kSms * (D == 128 ? 1 : 2);
-    const long long keys = static_cast<long long>(nb) * B;
+    const long long places = kSms * (D == 128 || wide ? 1 : 2);
     c.cluster = 1;
-    if (c.units >= 8 * places) return c;
-    if (keys <= 2048 || (keys <= 8192 && c.units * 8 <= places)) {
+    if (c.units >= 8 * places || (wide && keys <= 1024)) return c;
+    if (!wide && (keys <= 2048 || (keys <= 8192 && c.units * 8 <= places))) {
         const int warps = D == 128 && c.nt == 1 ? 12 : 8;
         while (c.cluster < 8 && c.cluster * warps < keys / calib::kChunk && c.units * c.cluster * 2 <= places) c.cluster *= 2;
         c.grid = c.units * c.cluster;
     } else {
-        const long long total = S * (keys / calib::kChunk + calib::kUnitCost), warps = D == 128 && c.nt == 1 ? 12 : 8;
+        const long long total = wide ? S * (keys / calib::kWideKeys + calib::kWideCost) : S * (keys / calib::kChunk + calib::kUnitCost);
+        const long long warps = wide ? 1 : (D == 128 && c.nt == 1 ? 12 : 8), least = wide ? calib::kWideMinShare : calib::kMinShare;
         double best = 0.;
-        for (long long shares = 1; shares <= std::max(1ll, 3 * places / columns) && shares <= std::max(1ll, total / calib::kMinShare);
+        for (long long shares = 1; shares <= std::max(1ll, 3 * places / columns) && shares <= std::max(1ll, total / least);
              ++shares) {
             const double cost = static_cast<double>(cdiv(shares * columns, places)) *
                                 (static_cast<double>(total) / static_cast<double>(shares * warps) + 6.);
@@ -526,8 +538,30 @@ calib_status launch_cached(const CUtensorMap& tk, const CUtensorMap& tv, const c
 }
 
 template <int D, int B>
+calib_status launch_wide(const CUtensorMap& tk, const CUtensorMap& tv, const calib::CachedParams& p, const CachedPlan& c,
+                         cudaStream_t st) {
+    using L = calib::WideSmem<D>;
+    static_assert(L::BYTES <= 232448, "shared memory budget");
+    auto* fn = calib::cached_wide_kernel<D, B>;
+    if (calib_status s = ensure_smem(reinterpret_cast<const void*>(fn), L::BYTES)) return s;
+    // the split of the registers waits for ones that the launch does not bring along
+    static std::atomic<bool> enough{false};
+    if (!enough) {
+        cudaFuncAttributes a{};
+        if (cudaFuncGetAttributes(&a, fn) != cudaSuccess || a.numRegs != calib::kWideRegs) return CALIB_ERR_CUDA;
+        enough = true;
+    }
+    if (calib_status s = launch_with(fn, static_cast<int>(c.grid), calib::kWideThreads, L::BYTES, st, 1, false, tk, tv, p))
+        return s;
+    if (!p.flat) return CALIB_OK;
+    constexpr int NT = calib::kWideRows / 8;
+    return launch_with(calib::cached_combine_kernel<D, NT>, static_cast<int>(c.units) * NT, 256, 0, st, 1, true, p);
+}
+
+template <int D, int B>
 calib_status launch_cached_nt(const CUtensorMap& tk, const CUtensorMap& tv, const calib::CachedParams& p,
                               const CachedPlan& c, cudaStream_t st) {
+    if (c.nt > 2) return launch_wide<D, B>(tk, tv, p, c, st);
     return c.nt == 1 ? launch_cached<D, B, 1>(tk, tv, p, c, st) : launch_cached<D, B, 2>(tk, tv, p, c, st);
 }
 

@@ -264,11 +264,11 @@ __device__ __forceinline__ float row_lse(float m, float l) {
 }
 
 // One cell: sequence s, K/V head h.  Its length and new tokens (0 where they are out of range), and the number
-// of 32-key chunks of the blocks that its query heads attend to.
+// of CK-key chunks of the blocks that its query heads attend to.
 struct CachedCell {
     int s, h, len, n_new, list0, chunks;
 };
-template <int B>
+template <int B, int CK = kChunk>
 __device__ __forceinline__ CachedCell cached_cell(const CachedParams& p, int s, int h) {
     CachedCell c;
     c.s = s;
@@ -290,7 +290,7 @@ __device__ __forceinline__ CachedCell cached_cell(const CachedParams& p, int s, 
             blocks = 0;
         }
     }
-    c.chunks = blocks * (B / kChunk);
+    c.chunks = blocks * (B / CK);
     return c;
 }
 
@@ -313,8 +313,8 @@ __device__ __forceinline__ CachedCell cached_cell(const CachedParams& p, int s, 
 //
 // Rows are few, so they are the N of the products and the keys their M: S^T = K Q^T and
 // O^T = V^T P^T as 16x8x16 MMAs, which wastes nothing at 8 rows where rows as M would fill half of a
-// tile.  (A tcgen05 tile has 128 rows in M; with keys there it would need the 8-bit operands
-// rewritten as 16-bit ones in shared memory first.)
+// tile.  (A tcgen05 tile has 128 rows in M, and needs the 8-bit operands rewritten as 16-bit ones in shared memory
+// first: cached_wide_kernel does that for many rows.)
 //   - e4m3 is exact in half precision: by the conversion instruction, except half of V at D = 128, where integer
 //     instructions share the work (4 x 131072 tokens: 178 us without that, 171 with; at D = 64, 34 without
 //     and 37 with, on 8 x 32760 tokens at 30%).  The NaNs of that half are looked for apart, and make their chunk's
@@ -857,6 +857,9 @@ __global__ void __launch_bounds__(256) cached_combine_kernel(const __grid_consta
     constexpr int RW = 8 * NT, PER = D / 32;
     wait_for_previous_launch();
     const int unit = static_cast<int>(blockIdx.x) / NT, r0 = (static_cast<int>(blockIdx.x) - unit * NT) * 8;
+    const int cell = unit / p.tiles, tile = unit - cell * p.tiles;
+    const int s = cell / p.Hkv, h = cell - s * p.Hkv;
+    if (tile * RW + r0 >= p.G * p.M) return;                // no row of these 8
     const int2 pc = p.pieces[unit];
     if (pc.y <= 0) return;
     __shared__ float2 top[8];                               // a row's maximum and its sum
@@ -897,8 +900,6 @@ __global__ void __launch_bounds__(256) cached_combine_kernel(const __grid_consta
 #pragma unroll
         for (int e = 0; e < PER; ++e) part[warp][r][lane * PER + e] = acc[r][e];
     __syncthreads();
-    const int cell = unit / p.tiles, tile = unit - cell * p.tiles;
-    const int s = cell / p.Hkv, h = cell - s * p.Hkv;
     const int row0 = tile * RW + r0;
     const size_t out_row = (static_cast<size_t>(s) * p.Hq + static_cast<size_t>(h) * p.G) * p.M + row0;
     for (int idx = threadIdx.x; idx < 8 * D / 2; idx += 256) {

@@ -1,0 +1,624 @@
+// Attention over the 8-bit cache for many query rows: prompts in pieces, several new tokens times
+// several heads of a group.  Up to 16 rows cached_attn_kernel reads the cache once and is bound by that;
+// beyond, it converts every key and value once per 16 rows, and the work on them bounds it (about 150 TFLOP/s).
+// Here 128 rows share a conversion, and the products are tcgen05 MMAs: 4 sequences of 16384 keys, 8 K/V heads, D = 128,
+// 128 rows: 84 us (410 TFLOP/s) against 248; 64 rows, 65536 keys: 242 against 430.
+//
+// What bounds it is the chain of a tile: the softmax of 64 columns takes its warps about 3700 cycles, two groups of them
+// in turn, a K tile's conversion 1400, at half of the instruction issue.  One issuer for both products, one group of
+// warps converting K and V, and one softmax group: 104 us at the 128 rows above.  Moving m' with every new maximum, which
+// rescales O in half of the tiles: 97.  All loads of a conversion before its stores, and four chains for the maximum and
+// the sum: 84 to 86.  Rings of six: 87.
+//
+// Per tile of 64 keys: S = Q K^T (TS, M = 128 rows, N = 64), P = 2^(x - m) (online softmax), O += P' V (TS, N = D).
+//   - e4m3 is exact in half precision, which all operands are in: K and V are converted from TMA's tiles
+//     into MMA tiles in shared memory, Q is scaled by a power of two per row as in cached_attn_kernel.
+//   - A block's value scale cannot be applied to an accumulator that all blocks share, so it goes into the
+//     weights: P' = 2^(x + log2 scale_v - m' + 11), with m' within 4 of the maximum of x + log2 scale_v over the
+//     row so far, and O is kept relative to m'.  The normaliser l = sum 2^(x - m) has its own maximum m.  Both come from one
+//     exponential: P' = 2^(x - m) 2^(log2 scale_v + m - m' + 11), the second factor one per row and tile.
+//     The result is O 2^(m' - m) / l; scales of any size, and 0, keep their meaning.
+// Two softmax warpgroups take alternate tiles, each with its own m, m', l and O, which meet at a segment's end.
+// Tensor memory, two of each: S (64 columns), P' (32 columns of pairs), O (D); and Q (D / 2).
+//   warp 0       TMA: 8-bit K and V tiles through a ring of four
+//   warps 1, 2   MMA issuers of S and of P' V: an MMA takes its issuer about 40 cycles, longer than the product itself
+//   warps 4-7    conversion: Q at a segment's start, then K tiles through a ring of two
+//   warps 8-11   conversion of V tiles, likewise
+//   warps 12-19  softmax and output, a row a thread in each group
+// Sequences are cut into shares as in cached_attn_kernel (a unit's own cost is 12 tiles here); every role walks the
+// same segments and looks its tiles up itself.
+#pragma once
+#include "attn_fwd.cuh"
+#include "kv_cache.cuh"
+
+namespace calib {
+
+constexpr int kWideThreads = 640;
+// Registers a thread: launched with 96 (five warpgroups of 128 threads), then shared out: 48 + 2 * 80 + 2 * 136 = 480.
+constexpr int kWideRegs = 96, kWideRegsIssue = 48, kWideRegsConvert = 80, kWideRegsSoftmax = 136;
+static_assert(kWideRegsIssue + 2 * kWideRegsConvert + 2 * kWideRegsSoftmax <= 5 * kWideRegs, "register split");
+template <int N> __device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N> __device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+constexpr int kWideRows = 128;
+constexpr int kWideKeys = 64;
+constexpr int kWideCost = 12;             // a unit's own cost in tiles; 6 and 8 measured within 2%
+constexpr int kWideMinShare = 24;         // no CTA gets less than this (a unit's own cost included)
+constexpr float kWideSlack = 4.f;         // P' is 2^(x + log2 scale_v - m' + 11), m' up to 4 below the maximum
+constexpr uint32_t kWideP = 128, kWideQ = 192, kWideO = 256;   // tensor-memory columns; S at 0 and 64, P' 32, O 128 apart
+
+template <int D>
+struct WideSmem {
+    static constexpr int CH = D / 64, ST8 = 4;
+    static constexpr uint32_t T8 = kWideKeys * D;                     // an 8-bit tile
+    static constexpr uint32_t CHUNK = kWideKeys * 128;                // 64 columns of a 16-bit tile
+    static constexpr uint32_t T16 = CH * CHUNK;
+    static constexpr uint32_t QCHUNK = kWideRows * 128;
+    static constexpr uint32_t OFF_8 = 0;                              // K and V, ST8 stages
+    static constexpr uint32_t OFF_K = OFF_8 + ST8 * 2 * T8, OFF_V = OFF_K + 2 * T16;
+    static constexpr uint32_t OFF_Q = OFF_V + 2 * T16;
+    static constexpr uint32_t OFF_FAC = OFF_Q + CH * QCHUNK;          // float [128]: Q's row factors
+    static constexpr uint32_t OFF_STAT = OFF_FAC + kWideRows * 4;     // float4 [2][2 groups][128]: m, m', l, any tile
+    static constexpr uint32_t OFF_BAR = OFF_STAT + 4 * kWideRows * 16;
+    static constexpr int B_8F = 0, B_8E = B_8F + ST8, B_KF = B_8E + ST8, B_VF = B_KF + 2, B_QF = B_VF + 2,
+                         B_QE = B_QF + 1, B_SF = B_QE + 1, B_SE = B_SF + 2, B_PF = B_SE + 2, B_O = B_PF + 2,
+                         B_STAT = B_O + 2, B_EPI = B_STAT + 1, B_DRAIN = B_EPI + 1, NBARS = B_DRAIN + 2;
+    static constexpr uint32_t OFF_SCAN = OFF_BAR + NBARS * 8;         // long long [warps], int [2]
+    static constexpr uint32_t OFF_MISC = OFF_SCAN + (kWideThreads / 32) * 8 + 8;
+    static constexpr uint32_t RAW = OFF_MISC + 16 + 1024;
+    static constexpr uint32_t BYTES = RAW > 120u * 1024 ? RAW : 120u * 1024;   // one CTA (all tensor memory) per SM
+};
+
+// A CTA's share of its column (K/V head and row tile), segment by segment: the part [c0, c1) of a unit's tiles.
+template <int B>
+struct WideShare {
+    const CachedParams& p;
+    int head, tile, share, shares, seq, v0, c0, c1;
+    long long total, left, pos;
+    CachedCell cl;
+    bool first;
+
+    __device__ __forceinline__ void cut() {
+        const int take = static_cast<int>(min(left, static_cast<long long>(cl.chunks + kWideCost - v0)));
+        c0 = min(v0, cl.chunks);
+        c1 = min(v0 + take, cl.chunks);
+        left -= take;
+    }
+    __device__ __forceinline__ bool next() {
+        if (!p.flat) return false;
+        pos += cl.chunks + kWideCost - v0;
+        v0 = 0;
+        first = false;
+        if (left <= 0) return false;
+        cl = cached_cell<B, kWideKeys>(p, ++seq, head);
+        cut();
+        return true;
+    }
+    // All threads of the CTA.  False: nothing falls to this CTA.
+    __device__ __forceinline__ bool init(uint8_t* scan) {
+        const int columns = p.Hkv * p.tiles, column = static_cast<int>(blockIdx.x) % columns;
+        const int warp = static_cast<int>(warp_id()), lane = static_cast<int>(lane_id());
+        head = column / p.tiles;
+        tile = column % p.tiles;
+        share = static_cast<int>(blockIdx.x) / columns;
+        shares = 1;
+        total = left = pos = 0;
+        v0 = 0;
+        first = true;
+        if (!p.flat) {
+            seq = share;
+            cl = cached_cell<B, kWideKeys>(p, seq, head);
+            c0 = 0;
+            c1 = cl.chunks;
+            return true;
+        }
+        long long* sums = reinterpret_cast<long long*>(scan);
+        int* start = reinterpret_cast<int*>(scan + kWideThreads / 32 * 8);
+        const int per = (p.S + kWideThreads - 1) / kWideThreads;
+        const int lo = min(p.S, static_cast<int>(threadIdx.x) * per), hi = min(p.S, lo + per);
+        long long mine = 0;
+        for (int x = lo; x < hi; ++x) mine += cached_cell<B, kWideKeys>(p, x, head).chunks + kWideCost;
+        long long incl = mine;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const long long y = __shfl_up_sync(0xffffffffu, incl, off);
+            if (lane >= off) incl += y;
+        }
+        if (lane == 31) sums[warp] = incl;
+        __syncthreads();
+        for (int w = 0; w < kWideThreads / 32; ++w) {
+            if (w < warp) incl += sums[w];
+            total += sums[w];
+        }
+        shares = static_cast<int>(min(static_cast<long long>(p.flat), max(1ll, total / kWideMinShare)));
+        if (share >= shares) return false;
+        pos = total * share / shares;
+        left = total * (share + 1) / shares - pos;
+        if (pos >= incl - mine && pos < incl) {
+            long long at = incl - mine;
+            for (int x = lo; x < hi; ++x) {
+                const int n = cached_cell<B, kWideKeys>(p, x, head).chunks + kWideCost;
+                if (pos < at + n) {
+                    start[0] = x;
+                    start[1] = static_cast<int>(pos - at);
+                    break;
+                }
+                at += n;
+            }
+        }
+        __syncthreads();
+        seq = start[0];
+        v0 = start[1];
+        cl = cached_cell<B, kWideKeys>(p, seq, head);
+        cut();
+        return !(v0 > 0 && c0 == c1 && !next_first());
+    }
+    // The share begins in a unit's own cost: nothing to do there.
+    __device__ __forceinline__ bool next_first() {
+        const bool more = next();
+        first = true;
+        return more;
+    }
+    __device__ __forceinline__ bool whole() const { return c0 == 0 && c1 == cl.chunks; }
+    __device__ __forceinline__ int slot() const { return 2 * static_cast<int>(blockIdx.x) + (first ? 0 : 1); }
+};
+
+// Tiles of a segment as a warp looks them up, one per lane and 32 at a time.  live(n): tile n has keys in the cache.
+template <int B>
+struct WideLook {
+    int y, key;
+    float ks, vs, lv;                                      // lv = log2 |vs|
+    uint32_t mask;
+    __device__ __forceinline__ void at(const CachedParams& p, const WideShare<B>& sh, int n0, bool report) {
+        constexpr int CPB = B / kWideKeys;
+        const int c = n0 + static_cast<int>(lane_id());
+        y = -1;
+        key = 0;
+        ks = vs = lv = 0.f;
+        if (c < sh.c1) {
+            int blk = c / CPB;
+            if (p.row_ptr) blk = p.col_idx[sh.cl.list0 + blk];
+            key = blk * B + c % CPB * kWideKeys;
+            if (blk >= 0 && key < sh.cl.len) {
+                const int page = p.table[static_cast<size_t>(sh.cl.s) * p.nb + blk];
+                if (page >= 0 && page < p.pages) {
+                    const int cell = page * p.Hkv + sh.cl.h;
+                    y = cell * B + c % CPB * kWideKeys;
+                    ks = p.k_scale[cell];
+                    vs = p.v_scale[cell];
+                    lv = log2f(fabsf(vs));
+                } else if (report) {
+                    raise_status(STATUS_BAD_CACHE);
+                }
+            }
+        }
+        mask = __ballot_sync(0xffffffffu, y >= 0);
+    }
+    __device__ __forceinline__ bool live(int n, int c0) const { return (mask >> ((n - c0) & 31)) & 1u; }
+};
+
+// One arrival for a warp, after what all its threads did.
+__device__ __forceinline__ void warp_arrive(uint32_t bar) {
+    __syncwarp();
+    if (lane_id() == 0) mbar_arrive(bar);
+}
+
+template <int D, int B>
+__global__ void __launch_bounds__(kWideThreads, 1)
+cached_wide_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                   const __grid_constant__ CachedParams p) {
+    using L = WideSmem<D>;
+    constexpr int ST8 = L::ST8;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    const uint32_t sbase = smem_u32(smem), bar0 = sbase + L::OFF_BAR;
+    auto bar = [&](int idx) -> uint32_t { return bar0 + 8u * idx; };
+    float* qfac = reinterpret_cast<float*>(smem + L::OFF_FAC);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::OFF_MISC);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::OFF_MISC + 4);
+    const int warp = static_cast<int>(warp_id()), lane = static_cast<int>(lane_id());
+
+    WideShare<B> sh{p};
+    if (!sh.init(smem + L::OFF_SCAN)) return;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < ST8; ++i) {
+            mbar_init(bar(L::B_8F + i), 1);
+            mbar_init(bar(L::B_8E + i), 8);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(bar(L::B_KF + i), 4);
+            mbar_init(bar(L::B_VF + i), 4);
+            mbar_init(bar(L::B_SF + i), 1);
+            mbar_init(bar(L::B_SE + i), 4);
+            mbar_init(bar(L::B_PF + i), 4);
+            mbar_init(bar(L::B_O + i), 1);
+        }
+        mbar_init(bar(L::B_QF), 4);
+        mbar_init(bar(L::B_QE), 9);
+        mbar_init(bar(L::B_STAT), 8);
+        mbar_init(bar(L::B_EPI), 8);
+        mbar_init(bar(L::B_DRAIN), 1);
+        mbar_init(bar(L::B_DRAIN + 1), 1);
+        *abort_flag = 0;
+        fence_barrier_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(smem_u32(tmem_slot), 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const WaitCtl ctl{abort_flag, p.timeout_ns};
+    const int rows = p.G * p.M, row0 = sh.tile * kWideRows;
+    int armed = 0;
+    bool ok = true;
+    WideLook<B> look;
+
+    // Every role: segments, and their live tiles counted through (u).
+    if (warp < 4) {
+        regs_down<kWideRegsIssue>();
+        if (warp == 0) {
+            // ===================== TMA producer =============================================
+            int u = 0;
+            do {
+                if (p.flat && sh.c0 == 0 && sh.v0 == 0 && lane == 0) {
+                    // the share that holds the unit's last tile is the last one that begins at or before it
+                    const long long last = sh.pos + sh.cl.chunks - 1;
+                    const int g1 = static_cast<int>(((last + 1) * sh.shares + sh.total - 1) / sh.total) - 1;
+                    p.pieces[(static_cast<size_t>(sh.cl.s) * p.Hkv + sh.cl.h) * p.tiles + sh.tile] =
+                        sh.whole() ? make_int2(0, 0) : make_int2(sh.slot(), g1 - sh.share + 1);
+                }
+                __syncwarp();
+                for (int n = sh.c0; ok && n < sh.c1; ++n) {
+                    if (((n - sh.c0) & 31) == 0) look.at(p, sh, n, true);
+                    if (!look.live(n, sh.c0)) continue;
+                    const int y = __shfl_sync(0xffffffffu, look.y, (n - sh.c0) & 31), s = u % ST8;
+                    if (!(ok = mbar_wait_warp(bar(L::B_8E + s), ((u / ST8) & 1) ^ 1, ctl))) break;
+                    if (elect_one()) {
+                        mbar_arrive_expect_tx(bar(L::B_8F + s), 2 * L::T8);
+                        for (int b = 0; b < kWideKeys; b += kChunk) {
+                            tma_load_2d(sbase + L::OFF_8 + s * 2 * L::T8 + b * D, &tm_k, bar(L::B_8F + s), 0, y + b);
+                            tma_load_2d(sbase + L::OFF_8 + s * 2 * L::T8 + L::T8 + b * D, &tm_v, bar(L::B_8F + s), 0, y + b);
+                        }
+                    }
+                    armed = ++u;
+                }
+            } while (ok && sh.next());
+        } else if (warp == 1) {
+            // ===================== issuer of S ==============================================
+            // kind::f16 with half-precision operands and fp32 sums (format fields 0), M = 128
+            constexpr uint32_t idesc = (1u << 4) | (static_cast<uint32_t>(kWideKeys >> 3) << 17) | (8u << 24);
+            int u = 0, segs = 0;
+            do {
+                // Q: converted; the previous segment's products with the old one are done
+                ok = mbar_wait_warp(bar(L::B_QF), segs & 1, ctl);
+                if (ok && u > 0) ok = mbar_wait_warp(bar(L::B_SF + ((u - 1) & 1)), ((u - 1) >> 1) & 1, ctl);
+                if (!ok) break;
+                tc_fence_after();
+                if (elect_one()) {
+    #pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk)
+                        tmem_cp_128x256b(tmem + kWideQ + kk * 8,
+                                         smem_desc_sw128(sbase + L::OFF_Q + (kk >> 2) * L::QCHUNK + (kk & 3) * 32, 16, 1024));
+                    umma_commit(bar(L::B_QE));
+                }
+                ++segs;
+                for (int n = sh.c0; n < sh.c1; ++n) {
+                    if (((n - sh.c0) & 31) == 0) look.at(p, sh, n, false);
+                    if (!look.live(n, sh.c0)) continue;
+                    const int b = u & 1;
+                    ok = mbar_wait_warp(bar(L::B_KF + b), (u >> 1) & 1, ctl);
+                    if (ok && u >= 2) ok = mbar_wait_warp(bar(L::B_SE + b), ((u >> 1) - 1) & 1, ctl);
+                    if (!ok) break;
+                    tc_fence_after();
+                    if (elect_one()) {
+                        const uint64_t kd = smem_desc_sw128(sbase + L::OFF_K + b * L::T16, 16, 1024);
+    #pragma unroll
+                        for (int kk = 0; kk < D / 16; ++kk)
+                            umma_ts(tmem + b * 64, tmem + kWideQ + kk * 8, kd + (((kk >> 2) * L::CHUNK + (kk & 3) * 32) >> 4), idesc,
+                                    kk > 0 ? 1u : 0u);
+                        umma_commit(bar(L::B_SF + b));         // S is there, and its K tile free
+                    }
+                    ++u;
+                }
+            } while (ok && sh.next());
+        } else if (warp == 2) {
+            // ===================== issuer of P' V ===========================================
+            constexpr uint32_t idesc = (1u << 4) | (1u << 16) | (static_cast<uint32_t>(D >> 3) << 17) | (8u << 24);
+            int u = 0, live_segs = 0;
+            do {
+                int done = 0;
+                for (int n = sh.c0; n < sh.c1; ++n) {
+                    if (((n - sh.c0) & 31) == 0) look.at(p, sh, n, false);
+                    if (!look.live(n, sh.c0)) continue;
+                    const int b = u & 1;
+                    ok = mbar_wait_warp(bar(L::B_VF + b), (u >> 1) & 1, ctl);
+                    if (ok) ok = mbar_wait_warp(bar(L::B_PF + b), (u >> 1) & 1, ctl);
+                    // the previous segment's output is read before the first product that overwrites it
+                    if (ok && done == 0 && live_segs > 0) ok = mbar_wait_warp(bar(L::B_EPI), (live_segs - 1) & 1, ctl);
+                    if (!ok) break;
+                    tc_fence_after();
+                    if (elect_one()) {
+                        const uint64_t vd = smem_desc_sw128(sbase + L::OFF_V + b * L::T16, L::CHUNK, 1024);
+    #pragma unroll
+                        for (int kk = 0; kk < kWideKeys / 16; ++kk)
+                            umma_ts(tmem + kWideO + b * 128, tmem + kWideP + b * 32 + kk * 8, vd + (kk * 16 * 128 >> 4), idesc,
+                                    (done > 1 || kk > 0) ? 1u : 0u);
+                        umma_commit(bar(L::B_O + b));          // O holds the tile, and its V and P are free
+                    }
+                    ++u;
+                    ++done;
+                }
+                if (done > 0) ++live_segs;
+            } while (ok && sh.next());
+        }
+    } else if (warp < 12) {
+        regs_down<kWideRegsConvert>();
+        // ===================== conversion ================================================
+        const bool is_v = warp >= 8;
+        const int t = static_cast<int>(threadIdx.x) & 127;
+        int u = 0, segs = 0;
+        // one 8-bit tile -> 16-bit MMA tile (rows of 128 bytes, 128-byte swizzle); rows from `rows_ok` on become zeros
+        auto convert = [&](uint32_t src, uint32_t dst, int rows_ok) {
+            constexpr int UPR = D / 16;                    // 16-value units per row
+#pragma unroll
+            for (int i = 0; i < kWideKeys * UPR / 128; ++i) {
+                const int x = t + i * 128, row = x / UPR, unit = x % UPR;
+                uint4 w;
+                if constexpr (D == 128) w = lds128(src + row * 128 + ((unit ^ (row & 7)) << 4));
+                else w = lds128(src + row * 64 + ((unit ^ ((row >> 1) & 3)) << 4));
+                if (rows_ok < kWideKeys && row >= rows_ok) w = make_uint4(0, 0, 0, 0);
+                const uint4 lo = make_uint4(e4m3x2_to_f16x2(w.x), e4m3x2_hi_to_f16x2(w.x), e4m3x2_to_f16x2(w.y), e4m3x2_hi_to_f16x2(w.y));
+                const uint4 hi = make_uint4(e4m3x2_to_f16x2(w.z), e4m3x2_hi_to_f16x2(w.z), e4m3x2_to_f16x2(w.w), e4m3x2_hi_to_f16x2(w.w));
+                const uint32_t base = dst + (unit >> 2) * L::CHUNK + row * 128;
+                const int j = (unit & 3) * 2, swap = unit >> 2;   // the second chunk's halves in the other order: no bank twice
+                const uint32_t a0 = base + (((j + swap) ^ (row & 7)) << 4), a1 = base + (((j + 1 - swap) ^ (row & 7)) << 4);
+                const uint4 f0 = swap ? hi : lo, f1 = swap ? lo : hi;
+                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a0), "r"(f0.x), "r"(f0.y), "r"(f0.z), "r"(f0.w) : "memory");
+                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a1), "r"(f1.x), "r"(f1.y), "r"(f1.z), "r"(f1.w) : "memory");
+            }
+        };
+        do {
+            // Q: a row a thread, scaled by a power of two into half precision.  The last segment's Q is in tensor memory, and
+            // the softmax warps have its factors: nobody is two segments behind, whose wait for B_QF would miss a phase.
+            if (!is_v && segs > 0 && !(ok = mbar_wait_warp(bar(L::B_QE), (segs - 1) & 1, ctl))) break;
+            if (!is_v) {
+                const int row = row0 + t;
+                const bool is = row < rows;
+                const __nv_bfloat16* src =
+                    p.q + ((static_cast<size_t>(sh.cl.s) * p.Hq + static_cast<size_t>(sh.cl.h) * p.G) * p.M + row) * D;
+                float amax = 0.f;
+#pragma unroll 4
+                for (int c = 0; c < D / 8; ++c) {
+                    const uint4 w = is ? *reinterpret_cast<const uint4*>(src + c * 8) : make_uint4(0, 0, 0, 0);
+                    const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(x[i] << 16)), fabsf(__uint_as_float(x[i] & 0xFFFF0000u))));
+                }
+                const int ef = max(15, min(254, static_cast<int>(__float_as_uint(amax) >> 23)));
+                const float up = __uint_as_float(static_cast<uint32_t>(268 - ef) << 23);
+                qfac[t] = __uint_as_float(static_cast<uint32_t>(ef - 14) << 23);
+#pragma unroll 4
+                for (int c = 0; c < D / 8; ++c) {
+                    const uint4 w = is ? *reinterpret_cast<const uint4*>(src + c * 8) : make_uint4(0, 0, 0, 0);
+                    const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+                    uint32_t f[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) f[i] = pack_f16x2(__uint_as_float(x[i] << 16) * up, __uint_as_float(x[i] & 0xFFFF0000u) * up);
+                    const uint32_t a = sbase + L::OFF_Q + (c >> 3) * L::QCHUNK + t * 128 + (((c & 7) ^ (t & 7)) << 4);
+                    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(f[0]), "r"(f[1]), "r"(f[2]), "r"(f[3]) : "memory");
+                }
+                fence_proxy_async_smem();
+                warp_arrive(bar(L::B_QF));
+            }
+            ++segs;
+            for (int n = sh.c0; ok && n < sh.c1; ++n) {
+                if (((n - sh.c0) & 31) == 0) look.at(p, sh, n, false);
+                if (!look.live(n, sh.c0)) continue;
+                const int key0 = __shfl_sync(0xffffffffu, look.key, (n - sh.c0) & 31);
+                const int s = u % ST8, b = u & 1;
+                const uint32_t src = sbase + L::OFF_8 + s * 2 * L::T8;
+                ok = mbar_wait_warp(bar(L::B_8F + s), (u / ST8) & 1, ctl);
+                if (ok) ok = mbar_wait_warp(bar((is_v ? L::B_O : L::B_SF) + b), ((u >> 1) & 1) ^ 1, ctl);
+                if (!ok) break;
+                // V: bytes behind the sequence can be anything
+                if (is_v && sh.cl.len - key0 < kWideKeys) convert(src + L::T8, sbase + L::OFF_V + b * L::T16, sh.cl.len - key0);
+                else convert(is_v ? src + L::T8 : src, sbase + (is_v ? L::OFF_V : L::OFF_K) + b * L::T16, kWideKeys);
+                fence_proxy_async_smem();
+                warp_arrive(bar((is_v ? L::B_VF : L::B_KF) + b));
+                warp_arrive(bar(L::B_8E + s));
+                ++u;
+            }
+        } while (ok && sh.next());
+    } else {
+        regs_up<kWideRegsSoftmax>();
+        // ===================== softmax and output ========================================
+        const uint32_t q4 = warp & 3;
+        const int grp = warp >= 16 ? 1 : 0;
+        float4* stat = reinterpret_cast<float4*>(smem + L::OFF_STAT);
+        const uint32_t to = tmem + ((q4 * 32) << 16) + kWideO, tp = tmem + ((q4 * 32) << 16) + kWideP + grp * 32;
+        const int r = static_cast<int>(q4 * 32) + lane;    // row of the tile == TMEM lane
+        const uint32_t lane_base = (q4 * 32) << 16;
+        const int row = row0 + r;
+        int u = 0, segs = 0;
+        do {
+            ok = mbar_wait_warp(bar(L::B_QF), segs & 1, ctl);     // the row factors
+            if (!ok) break;
+            const float fac = row < rows ? qfac[r] * p.scale_log2 : 1.f;
+            warp_arrive(bar(L::B_QE));
+            ++segs;
+            const int tok = row % p.M;
+            int limit = tok < sh.cl.n_new ? (p.causal ? sh.cl.len - sh.cl.n_new + tok + 1 : sh.cl.len) : 0;
+            if (row >= rows) limit = 0x7FFFFFFF;           // no row: nothing to mask, and nobody reads what comes out
+            float m = -INFINITY, mv = -INFINITY, l = 0.f;  // maxima of x and of x + log2 scale_v, sum of 2^(x - m)
+            int done = 0;
+            for (int n = sh.c0; ok && n < sh.c1; ++n) {
+                if (((n - sh.c0) & 31) == 0) look.at(p, sh, n, false);
+                if (!look.live(n, sh.c0)) continue;
+                if ((u & 1) != grp) {
+                    ++u;
+                    continue;
+                }
+                const int src = (n - sh.c0) & 31;
+                const int key0 = __shfl_sync(0xffffffffu, look.key, src);
+                float f = fac * __shfl_sync(0xffffffffu, look.ks, src);
+                const float vs = __shfl_sync(0xffffffffu, look.vs, src);
+                if (!(ok = mbar_wait_warp(bar(L::B_SF + grp), (u >> 1) & 1, ctl))) break;
+                tc_fence_after();
+                if (row0 + static_cast<int>(q4 * 32) >= rows) {   // a warp without rows: whatever its P holds, nobody reads its O
+                    warp_arrive(bar(L::B_SE + grp));
+                    if (done > 0 && !(ok = mbar_wait_warp(bar(L::B_O + grp), ((u >> 1) - 1) & 1, ctl))) break;
+                    warp_arrive(bar(L::B_PF + grp));
+                    ++u;
+                    ++done;
+                    continue;
+                }
+                uint32_t x[64];
+                tmem_ld64_wait(tmem + lane_base + grp * 64, x);
+                tc_fence_before();
+                warp_arrive(bar(L::B_SE + grp));           // S may be overwritten
+                auto val = [&](int c) { return __uint_as_float(x[c]); };
+                // logits are S f; where a key is masked, or a scale is not above 0, they are made here
+                if (__any_sync(0xffffffffu, key0 + kWideKeys > limit || !(f > 0.f))) {
+#pragma unroll
+                    for (int c = 0; c < 64; ++c) x[c] = key0 + c >= limit ? 0xFF800000u : __float_as_uint(val(c) * f);
+                    f = 1.f;
+                }
+                float mx = val(0);
+#pragma unroll
+                for (int c = 1; c + 1 < 64; c += 2) mx = fmax3(mx, val(c), val(c + 1));
+                mx = fmaxf(mx, val(63)) * f;
+                const float m_new = fmaxf(m, mx), m_ref = m_new == -INFINITY ? 0.f : m_new;
+                // m' is moved when the maximum passes it by 16 times: few tiles after the first do.  A negative scale weighs with
+                // its magnitude and gives its sign back.  Where the factor would pass 2^127 the tile's largest 2^(x - m) is
+                // below 2^-112, and the product still below 2^15.  A row that sees no key of the tile, or a block of
+                // zeros, has no weight.
+                const float lv = __shfl_sync(0xffffffffu, look.lv, src), top = mx + lv;
+                const float mv_new = top > mv + kWideSlack ? top : mv;
+                const float up = lv + m_ref - mv_new + (kPShift - kWideSlack);
+                const float w = mx == -INFINITY || vs == 0.f ? 0.f : copysignf(ex2_approx(up > 127.f ? 127.f : up), vs);
+                l *= m == -INFINITY ? 0.f : ex2_approx(m - m_ref);
+                // the group's previous P has been read by its product, and its O is complete up to it
+                if (done > 0 && !(ok = mbar_wait_warp(bar(L::B_O + grp), ((u >> 1) - 1) & 1, ctl))) break;
+                tc_fence_after();
+                const bool moved = done > 0 && mv_new > mv;
+                if (__any_sync(0xffffffffu, moved)) {
+                    const float a = !moved ? 1.f : (mv == -INFINITY ? 0.f : ex2_approx(mv - mv_new));
+#pragma unroll 1
+                    for (int c = 0; c < D; c += 16) {
+                        uint32_t raw[16];
+                        tmem_ld16_wait(to + grp * 128 + c, raw);
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) raw[e] = __float_as_uint(__uint_as_float(raw[e]) * a);
+                        tmem_st16(to + grp * 128 + c, raw);
+                    }
+                }
+                float l0 = 0.f, l1 = 0.f;
+#pragma unroll
+                for (int c = 0; c < 64; c += 32) {
+                    uint32_t pk[16];
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2) {
+                        float p0, p1, w0, w1;
+                        ffma2(p0, p1, val(c + e), val(c + e + 1), f, f, -m_ref, -m_ref);
+                        p0 = ex2_approx(p0);
+                        p1 = ex2_approx(p1);
+                        fadd2(l0, l1, l0, l1, p0, p1);
+                        fmul2(w0, w1, p0, p1, w, w);
+                        pk[e / 2] = pack_f16x2(w0, w1);
+                    }
+                    tmem_st16(tp + c / 2, pk);
+                }
+                l += l0 + l1;
+                tmem_wait_st();
+                tc_fence_before();
+                warp_arrive(bar(L::B_PF + grp));
+                m = m_new;
+                mv = mv_new;
+                ++u;
+                ++done;
+            }
+            // the group's last tile is u - 1 or u - 2
+            if (ok && done > 0) ok = mbar_wait_warp(bar(L::B_O + grp), ((u - 1 - ((u - 1 - grp) & 1)) >> 1) & 1, ctl);
+            if (!ok) break;
+            // The groups' results meet: each thread gives its row's statistics, then takes half of the columns of both.
+            // Two sets of them: who writes the next but one has seen everybody arrive at the next.
+            float4* st = stat + ((segs - 1) & 1) * 2 * kWideRows;
+            st[grp * kWideRows + r] = make_float4(m, mv, l, done > 0 ? 1.f : 0.f);
+            tc_fence_before();
+            warp_arrive(bar(L::B_STAT));
+            if (!(ok = mbar_wait_warp(bar(L::B_STAT), (segs - 1) & 1, ctl))) break;
+            tc_fence_after();
+            const float4 s0 = st[r], s1 = st[kWideRows + r];
+            m = fmaxf(s0.x, s1.x);
+            // O relative to m and to 2^-8, l relative to 2^(m - 15), as the parts of cached_attn_kernel are
+            l = (s0.z * merge_weight(s0.x, m) + s1.z * merge_weight(s1.x, m)) * 32768.f;
+            const bool whole = sh.whole();
+            const float f0 = 0.0625f * (whole ? out_factor(l) : 1.f);
+            const float fa = s0.y == -INFINITY || m == -INFINITY ? 0.f : exp2f(s0.y - m);
+            const float fb = s1.y == -INFINITY || m == -INFINITY ? 0.f : exp2f(s1.y - m);
+            const size_t at = (static_cast<size_t>(sh.cl.s) * p.Hq + static_cast<size_t>(sh.cl.h) * p.G) * p.M + row;
+            const size_t part = static_cast<size_t>(sh.slot()) * kWideRows + r;
+            const bool nan = l != l;                       // a NaN logit
+#pragma unroll 1
+            for (int cc = 0; cc < D / 2; cc += 16) {
+                const int c = grp * (D / 2) + cc;
+                uint32_t raw[16], other[16];
+                if (s0.w != 0.f) tmem_ld16_wait(to + c, raw);
+                if (s1.w != 0.f) tmem_ld16_wait(to + 128 + c, other);
+                if (row >= rows) continue;
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    float y = 0.f;
+                    if (s0.w != 0.f) y = __uint_as_float(raw[e]) * f0 * fa;
+                    if (s1.w != 0.f) y += __uint_as_float(other[e]) * f0 * fb;
+                    raw[e] = __float_as_uint(nan ? l : y);
+                }
+                if (!whole || p.out_f32) {
+                    float* dst = whole ? static_cast<float*>(p.o) + at * D + c : p.part_o + part * D + c;
+#pragma unroll
+                    for (int e = 0; e < 16; e += 4)
+                        *reinterpret_cast<uint4*>(dst + e) = make_uint4(raw[e], raw[e + 1], raw[e + 2], raw[e + 3]);
+                } else {
+                    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.o) + at * D + c;
+#pragma unroll
+                    for (int e = 0; e < 16; e += 8) {
+                        auto two = [&](int i) { return pack_bf16x2(__uint_as_float(raw[e + i]), __uint_as_float(raw[e + i + 1])); };
+                        *reinterpret_cast<uint4*>(dst + e) = make_uint4(two(0), two(2), two(4), two(6));
+                    }
+                }
+            }
+            if (row < rows && grp == 0) {
+                if (!whole) p.part_ml[part] = make_float2(m, l);
+                else if (p.lse) p.lse[at] = row_lse(m, l);
+            }
+            if (s0.w != 0.f || s1.w != 0.f) {              // the same in all threads
+                tc_fence_before();
+                warp_arrive(bar(L::B_EPI));                // O may be overwritten
+            }
+        } while (ok && sh.next());
+    }
+
+    // ---- teardown (also the abort drain) ----------------------------------------
+    __syncthreads();
+    if (*abort_flag) {
+        constexpr uint64_t kDrainNs = 1000000000ull;
+        if (warp == 0 && lane == 0)
+            for (int t = max(0, armed - ST8); t < armed; ++t) mbar_wait_drain(bar(L::B_8F + t % ST8), (t / ST8) & 1, kDrainNs);
+        if ((warp == 1 || warp == 2) && lane == 0) {
+            umma_commit(bar(L::B_DRAIN + warp - 1));
+            mbar_wait_drain(bar(L::B_DRAIN + warp - 1), 0, kDrainNs);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+}  // namespace calib

@@ -155,10 +155,29 @@ CASES = [
 ]
 
 
+# Many rows: a table that has room for long sequences, whose entries past the end name no page.
+ROOM = 8192
+WIDE = [
+    (1, 8, 1, 33, 128, 128, [5000], None, True, None),             # 264 rows: three tiles of 128, cut
+    (5, 8, 1, 16, 64, 64, [0, 3000, 17, 1, 900], [0, 16, 16, 1, 7], True, None),   # 128 rows, a sequence without keys
+    (3, 12, 2, 7, 128, 128, [2100, 900, 65], None, True, 0.3),     # 42 rows
+    (2, 2, 1, 75, 64, 128, [4000, 129], [75, 2], True, 0.5),       # 150 rows
+    (2, 3, 1, 11, 128, 64, [11, 1029], None, True, None),          # 33 rows
+    (2, 4, 2, 40, 128, 64, [40, 777], [40, 17], False, None),      # 80 rows, no causal limit
+    (3, 1, 1, 80, 64, 64, [80, 64, 6000], [80, 64, 1], True, 0.6),
+    (1, 5, 1, 200, 64, 128, [200], None, True, None),              # 1000 rows
+]
+
+
+def _with_room(table):
+    return torch.nn.functional.pad(table, (0, ROOM - table.shape[1]), value=2 ** 31 - 1)
+
+
 @pytest.mark.gpu
-@pytest.mark.parametrize("S,Hq,Hkv,M,D,B,lengths,new,causal,density", CASES)
+@pytest.mark.parametrize("S,Hq,Hkv,M,D,B,lengths,new,causal,density,room",
+                         [c + (False,) for c in CASES] + [c + (True,) for c in WIDE])
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
-def test_attention(S, Hq, Hkv, M, D, B, lengths, new, causal, density, dtype):
+def test_attention(S, Hq, Hkv, M, D, B, lengths, new, causal, density, room, dtype):
     rng = np.random.default_rng(sum(lengths) + D + M)
     nb = max(1, max(ops.nblocks(n, B) for n in lengths))
     cache, table = _cache(rng, S, Hkv, D, B, nb)
@@ -168,25 +187,28 @@ def test_attention(S, Hq, Hkv, M, D, B, lengths, new, causal, density, dtype):
         mask = (rng.random((Hkv, S, nb)) < density).astype(np.uint8)
         mask[0, 0] = 0                                             # a head that keeps nothing of a sequence
         mask[-1, -1, -1] = 1                                       # the block that ends inside
-        bl = ops.BlockList.from_mask(torch.from_numpy(mask).cuda(), B)
-    o, lse = ops.sparse_attn_cached(q, cache, table, _ints(lengths), blist=bl, causal=causal, out_dtype=dtype,
+        wide = np.pad(mask, ((0, 0), (0, 0), (0, ROOM - nb))) if room else mask
+        bl = ops.BlockList.from_mask(torch.from_numpy(wide).cuda(), B)
+    o, lse = ops.sparse_attn_cached(q, cache, _with_room(table) if room else table, _ints(lengths), blist=bl, causal=causal, out_dtype=dtype,
                                     new_lens=None if new is None else _ints(new), return_lse=True)
     ops.device_check()
     _check(o, lse, q, cache, table, lengths, [M] * S if new is None else new, D ** -0.5, causal, mask)
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("D", [64, 128])
-def test_anything_behind_the_end_and_in_unused_pages(D):
+@pytest.mark.parametrize("D,M", [(64, 2), (128, 2), (64, 40), (128, 40)])
+def test_anything_behind_the_end_and_in_unused_pages(D, M):
     """NaN and the largest values in the bytes behind each sequence's end, in unused pages and in their
     scales; table entries past the end name no page."""
     S, Hkv, B, nb = 2, 2, 64, 6
     lengths = [65, 200]
     rng = np.random.default_rng(D)
     cache, table = _cache(rng, S, Hkv, D, B, nb)
-    q = torch.randn(S, 4, 2, D, generator=torch.Generator().manual_seed(2)).to(torch.bfloat16).cuda()
-    clean = ops.sparse_attn_cached(q, cache, table, _ints(lengths), return_lse=True)
+    q = torch.randn(S, 4, M, D, generator=torch.Generator().manual_seed(2)).to(torch.bfloat16).cuda()
     used = {int(table[s, b]): min(B, lengths[s] - b * B) for s in range(S) for b in range(ops.nblocks(lengths[s], B))}
+    if M > 2:
+        table = _with_room(table)
+    clean = ops.sparse_attn_cached(q, cache, table, _ints(lengths), return_lse=True)
     kb, vb = cache.k.view(torch.uint8), cache.v.view(torch.uint8)
     for page in range(cache.k.shape[0]):
         n = used.get(page, 0)
@@ -203,13 +225,14 @@ def test_anything_behind_the_end_and_in_unused_pages(D):
 
 
 @pytest.mark.gpu
-def test_values_of_every_size():
+@pytest.mark.parametrize("M", [2, 70])
+def test_values_of_every_size(M):
     """Logits of +-200 from queries of 2^-60 and 2^60 against scales that undo it, weights down to 2^-35 of
     the largest, a scale of 0, and queries of 0."""
     S, H, D, B = 1, 4, 64, 64
     rng = np.random.default_rng(3)
     cache, table = _cache(rng, S, H, D, B, 8)
-    q = torch.randn(S, H, 2, D, generator=torch.Generator().manual_seed(3)) * 4
+    q = torch.randn(S, H, M, D, generator=torch.Generator().manual_seed(3)) * 4
     q[:, 0] *= 2.0 ** -60
     q[:, 1] *= 2.0 ** 60
     q[:, 2, 0] = 0
@@ -217,14 +240,45 @@ def test_values_of_every_size():
     cache.k_scale[:, 1] *= 2.0 ** -60
     cache.v_scale[int(table[0, 3]), 2] = 0.0
     q = q.to(torch.bfloat16).cuda()
-    o, lse = ops.sparse_attn_cached(q, cache, table, _ints([500]), return_lse=True, out_dtype=torch.float32)
+    o, lse = ops.sparse_attn_cached(q, cache, table if M == 2 else _with_room(table), _ints([500]), return_lse=True,
+                                    out_dtype=torch.float32)
     k, v, ks, vs = f8(cache.k), f8(cache.v), to64(cache.k_scale), to64(cache.v_scale)
-    O, L, A = oracle.cached_attention(to64(q), k, v, ks, vs, table.cpu().numpy(), [500], [2], D ** -0.5, True)
+    O, L, A = oracle.cached_attention(to64(q), k, v, ks, vs, table.cpu().numpy(), [500], [M], D ** -0.5, True)
     # e as above, head by head: |q||k| of each head's own sizes
     for h in range(H):
         e = (D + 8) * U32 * D ** -0.5 * float(np.abs(to64(q))[0, h].sum(-1).max()) * 448 * ks[:, h].max() + 2.0 ** -20
         assert np.all(np.abs(to64(o)[0, h] - O[0, h]) <= (2.0 ** -11 + 2 * e + 500 * U32) * A[0, h] + U32 * np.abs(O[0, h]))
         assert np.all(np.abs(to64(lse)[0, h] - L[0, h]) <= e + 500 * U32 + 2.0 ** -22 * (1 + np.abs(L[0, h])))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("M,n", [(1, 500), (20, 500), (70, 500), (70, 3000)])
+def test_value_scales_of_every_size(D, M, n):
+    """Blocks whose value scales are 2^-60 to 2^60, in every order along the sequence; the block with the largest
+    logits, for most rows more than 100 above the others, has a value scale of 0."""
+    S, H, B = 1, 2, 64
+    nb = ops.nblocks(n, B)
+    cache, table = _cache(np.random.default_rng(21), S, H, D, B, nb)
+    q = torch.randn(S, H, M, D, generator=torch.Generator().manual_seed(21)).to(torch.bfloat16).cuda()
+    sizes = torch.exp2(torch.linspace(-60, 60, nb)).cuda()
+    cache.v_scale[table[0].long(), 0] *= sizes
+    cache.v_scale[table[0].long(), 1] *= sizes.flip(0)
+    last = int(table[0, 2])
+    cache.k_scale[last, :] *= 64
+    cache.v_scale[last, :] = 0.0
+    o, lse = ops.sparse_attn_cached(q, cache, table if M < 70 else _with_room(table), _ints([n]), return_lse=True,
+                                    out_dtype=torch.float32)
+    ops.device_check()
+    k, v, ks, vs = f8(cache.k), f8(cache.v), to64(cache.k_scale), to64(cache.v_scale)
+    O, L, A = oracle.cached_attention(to64(q), k, v, ks, vs, table.cpu().numpy(), [n], [M], D ** -0.5, True)
+    used = table[0].cpu().numpy()
+    for h in range(H):
+        e = (D + 8) * U32 * D ** -0.5 * float(np.abs(to64(q))[0, h].sum(-1).max()) * 448 * ks[used, h].max() + 2.0 ** -20
+        # weights of 2^-39 of the row's largest and below may be lost: n of them, at the largest value
+        lost = n * 2.0 ** -39 * 448 * vs[used, h].max()
+        assert np.all(np.abs(to64(o)[0, h] - O[0, h]) <= (2.0 ** -11 + 2 * e + n * U32) * A[0, h] + U32 * np.abs(O[0, h]) + lost)
+        assert np.all(np.abs(to64(lse)[0, h] - L[0, h]) <= e + n * U32 + 2.0 ** -22 * (1 + np.abs(L[0, h])))
 
 
 @pytest.mark.gpu
@@ -375,11 +429,14 @@ def test_tokens_written_one_by_one_then_attended_to():
 
 
 @pytest.mark.gpu
-def test_same_bits_on_another_stream_and_replayed():
+@pytest.mark.parametrize("M", [1, 40])
+def test_same_bits_on_another_stream_and_replayed(M):
     S, Hq, Hkv, D, B = 2, 4, 2, 128, 64
     cache, table = _cache(np.random.default_rng(8), S, Hkv, D, B, 60)
     lengths = _ints([3800, 100])
-    q = torch.randn(S, Hq, 1, D, generator=torch.Generator().manual_seed(8)).to(torch.bfloat16).cuda()
+    q = torch.randn(S, Hq, M, D, generator=torch.Generator().manual_seed(8)).to(torch.bfloat16).cuda()
+    if M > 1:
+        table = _with_room(table)
     call = lambda: ops.sparse_attn_cached(q, cache, table, lengths, return_lse=True)
     first = call()
     side = torch.cuda.Stream()
@@ -450,24 +507,26 @@ def test_refusals_on_the_gpu():
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("D", [64, 128])
-def test_a_live_nan_is_not_hidden(D):
+@pytest.mark.parametrize("D,M", [(64, 1), (128, 1), (64, 70), (128, 70)])
+def test_a_live_nan_is_not_hidden(D, M):
     """NaN in a value (at every place of a word, each of which is converted in its own way) or in a key of a live
     token shows in the outputs that weigh it, and not in other heads or sequences."""
     S, H, B = 2, 2, 64
-    cache, table = _cache(np.random.default_rng(11), S, H, D, B, 2)
-    q = torch.randn(S, H, 1, D, generator=torch.Generator().manual_seed(11)).to(torch.bfloat16).cuda()
-    clean = ops.sparse_attn_cached(q, cache, table, _ints([100, 90]))
+    cache, table = _cache(np.random.default_rng(11), S, H, D, B, 3)
+    q = torch.randn(S, H, M, D, generator=torch.Generator().manual_seed(11)).to(torch.bfloat16).cuda()
     page = int(table[0, 1])
+    if M > 1:
+        table = _with_room(table)
+    clean = ops.sparse_attn_cached(q, cache, table, _ints([180, 175]))
     for d in range(8):
         for byte in (0x7F, 0xFF):
             bad = ops.KVCache(cache.k, cache.v.view(torch.uint8).clone().view(torch.float8_e4m3fn), cache.k_scale, cache.v_scale)
             bad.v.view(torch.uint8)[page, 1, 13, d] = byte
-            o = ops.sparse_attn_cached(q, bad, table, _ints([100, 90]))
-            assert torch.isnan(o[0, 1, 0, d]) and torch.equal(o[0, 0], clean[0, 0]) and torch.equal(o[1], clean[1])
+            o = ops.sparse_attn_cached(q, bad, table, _ints([180, 175]))
+            assert torch.isnan(o[0, 1, :, d]).all() and torch.equal(o[0, 0], clean[0, 0]) and torch.equal(o[1], clean[1])
             bad = ops.KVCache(cache.k.view(torch.uint8).clone().view(torch.float8_e4m3fn), cache.v, cache.k_scale, cache.v_scale)
             bad.k.view(torch.uint8)[page, 1, 13, d] = byte
-            o, lse = ops.sparse_attn_cached(q, bad, table, _ints([100, 90]), return_lse=True)
+            o, lse = ops.sparse_attn_cached(q, bad, table, _ints([180, 175]), return_lse=True)
             assert torch.isnan(o[0, 1]).all() and torch.isnan(lse[0, 1]).all() and torch.equal(o[1], clean[1])
 
 
@@ -478,7 +537,11 @@ def test_a_live_nan_is_not_hidden(D):
     (300, 2, 2, 1, 64, 64, 2300),         # long lines of short sequences: many units a share
     (2, 1, 1, 1, 128, 128, 9000),         # two sequences, one head: every share of one line
     (1, 4, 4, 1, 64, 128, 8192),          # clusters of 8
-    (3, 8, 4, 30, 128, 128, 2500)])       # several row tiles, cut
+    (3, 8, 4, 30, 128, 128, 2500),        # several row tiles, cut
+    (250, 8, 1, 10, 128, 64, 1500),       # 80 rows, long lines of short sequences
+    (40, 4, 2, 100, 64, 64, 2100),        # 200 rows, lines of sequences for each of two tiles
+    (2, 3, 1, 100, 128, 128, 40000),      # 300 rows, lines of two sequences
+    (20, 16, 4, 32, 128, 64, 1000)])      # 128 rows, a CTA each
 def test_every_way_of_sharing_the_work(S, Hq, Hkv, M, D, B, longest):
     """Ragged lengths from 0 up under a table for the longest, so that cuts fall everywhere: against each sequence
     alone in a call of its own (whose cuts are others), which the cases above hold to the oracle."""
