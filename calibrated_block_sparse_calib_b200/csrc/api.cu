@@ -444,7 +444,7 @@ calib_status bwd_common(const void* q, const void* k, const void* v, const void*
 // more for its start and end.
 //
 // cached_wide_kernel takes many query rows.  Its 128 rows cost what 2 tiles of 16 rows (4 at D = 64) cost
-// cached_attn_kernel (4 sequences of 65536 keys, 8 K/V heads: 242 against 228 us with 32 rows and 241 against 332 with
+// cached_attn_kernel (4 sequences of 65536 keys, 8 K/V heads: 242 against 220 us with 32 rows and 241 against 332 with
 // 40 at D = 128; 235 against 236 with 64 at D = 64), and about 10 us more to start and end, which 2^18 keys times tiles
 // saved (2^19 at D = 64) make up for: 2 x 1024 keys, 4 heads, 256 rows, 29 against 20 us; 16 x 2048 keys, 8 heads, 40
 // rows, 54 against 64.

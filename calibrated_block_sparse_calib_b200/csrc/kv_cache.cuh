@@ -724,12 +724,40 @@ cached_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
             // kept over 2^8
             float vs_mt[2] = {vs * 0.00390625f, vs * 0.00390625f};
             if constexpr (kShifted) vs_mt[0] = __any_sync(0xffffffffu, (nan & 0x8080u) != 0u) ? __int_as_float(0x7FC00000) : vs;
+            if constexpr (NT == 1 || D == 64) {
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+                for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int mt = 0; mt < MT; ++mt)
+                    for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) o[nt][mt][e] = o[nt][mt][e] * alpha[nt][e & 1] + oc[nt][mt][e] * vs_mt[mt & 1];
+                        for (int e = 0; e < 4; ++e) o[nt][mt][e] = o[nt][mt][e] * alpha[nt][e & 1] + oc[nt][mt][e] * vs_mt[mt & 1];
+            } else {
+                // Scaled only after a new maximum, and in pairs: 126 -> 122 us at 16 rows (4 x 65536 tokens, 8 heads), 227 -> 220
+                // at 32; at 8 rows 3% slower, at D = 64 the same.
+                bool moved = false;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) moved |= alpha[nt][0] != 1.f || alpha[nt][1] != 1.f;
+                if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int mt = 0; mt < MT; ++mt) {
+                            float(&x)[4] = o[nt][mt];
+                            fmul2(x[0], x[1], x[0], x[1], alpha[nt][0], alpha[nt][1]);
+                            fmul2(x[2], x[3], x[2], x[3], alpha[nt][0], alpha[nt][1]);
+                        }
+                }
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt) {
+                        float(&x)[4] = o[nt][mt];
+                        const float(&y)[4] = oc[nt][mt];
+                        const float w = vs_mt[mt & 1];
+                        ffma2(x[0], x[1], y[0], y[1], w, w, x[0], x[1]);
+                        ffma2(x[2], x[3], y[2], y[3], w, w, x[2], x[3]);
+                    }
+            }
         }
         it = (it + mine) % ST;
 
