@@ -298,7 +298,7 @@ cached_wide_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                 if (!ok) break;
                 tc_fence_after();
                 if (elect_one()) {
-    #pragma unroll
+#pragma unroll
                     for (int kk = 0; kk < D / 16; ++kk)
                         tmem_cp_128x256b(tmem + kWideQ + kk * 8,
                                          smem_desc_sw128(sbase + L::OFF_Q + (kk >> 2) * L::QCHUNK + (kk & 3) * 32, 16, 1024));
@@ -315,7 +315,7 @@ cached_wide_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                     tc_fence_after();
                     if (elect_one()) {
                         const uint64_t kd = smem_desc_sw128(sbase + L::OFF_K + b * L::T16, 16, 1024);
-    #pragma unroll
+#pragma unroll
                         for (int kk = 0; kk < D / 16; ++kk)
                             umma_ts(tmem + b * 64, tmem + kWideQ + kk * 8, kd + (((kk >> 2) * L::CHUNK + (kk & 3) * 32) >> 4), idesc,
                                     kk > 0 ? 1u : 0u);
@@ -342,7 +342,7 @@ cached_wide_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                     tc_fence_after();
                     if (elect_one()) {
                         const uint64_t vd = smem_desc_sw128(sbase + L::OFF_V + b * L::T16, L::CHUNK, 1024);
-    #pragma unroll
+#pragma unroll
                         for (int kk = 0; kk < kWideKeys / 16; ++kk)
                             umma_ts(tmem + kWideO + b * 128, tmem + kWideP + b * 32 + kk * 8, vd + (kk * 16 * 128 >> 4), idesc,
                                     (done > 1 || kk > 0) ? 1u : 0u);
@@ -569,27 +569,29 @@ cached_wide_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                 uint32_t raw[16], other[16];
                 if (s0.w != 0.f) tmem_ld16_wait(to + c, raw);
                 if (s1.w != 0.f) tmem_ld16_wait(to + 128 + c, other);
-                if (row >= rows) continue;
+                if (row < rows) {
 #pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    float y = 0.f;
-                    if (s0.w != 0.f) y = __uint_as_float(raw[e]) * f0 * fa;
-                    if (s1.w != 0.f) y += __uint_as_float(other[e]) * f0 * fb;
-                    raw[e] = __float_as_uint(nan ? l : y);
-                }
-                if (!whole || p.out_f32) {
-                    float* dst = whole ? static_cast<float*>(p.o) + at * D + c : p.part_o + part * D + c;
+                    for (int e = 0; e < 16; ++e) {
+                        float y = 0.f;
+                        if (s0.w != 0.f) y = __uint_as_float(raw[e]) * f0 * fa;
+                        if (s1.w != 0.f) y += __uint_as_float(other[e]) * f0 * fb;
+                        raw[e] = __float_as_uint(nan ? l : y);
+                    }
+                    if (!whole || p.out_f32) {
+                        float* dst = whole ? static_cast<float*>(p.o) + at * D + c : p.part_o + part * D + c;
 #pragma unroll
-                    for (int e = 0; e < 16; e += 4)
-                        *reinterpret_cast<uint4*>(dst + e) = make_uint4(raw[e], raw[e + 1], raw[e + 2], raw[e + 3]);
-                } else {
-                    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.o) + at * D + c;
+                        for (int e = 0; e < 16; e += 4)
+                            *reinterpret_cast<uint4*>(dst + e) = make_uint4(raw[e], raw[e + 1], raw[e + 2], raw[e + 3]);
+                    } else {
+                        __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.o) + at * D + c;
 #pragma unroll
-                    for (int e = 0; e < 16; e += 8) {
-                        auto two = [&](int i) { return pack_bf16x2(__uint_as_float(raw[e + i]), __uint_as_float(raw[e + i + 1])); };
-                        *reinterpret_cast<uint4*>(dst + e) = make_uint4(two(0), two(2), two(4), two(6));
+                        for (int e = 0; e < 16; e += 8) {
+                            auto two = [&](int i) { return pack_bf16x2(__uint_as_float(raw[e + i]), __uint_as_float(raw[e + i + 1])); };
+                            *reinterpret_cast<uint4*>(dst + e) = make_uint4(two(0), two(2), two(4), two(6));
+                        }
                     }
                 }
+                __syncwarp();                              // tensor-memory loads take the whole warp
             }
             if (row < rows && grp == 0) {
                 if (!whole) p.part_ml[part] = make_float2(m, l);
